@@ -19,19 +19,24 @@ _ROOT = os.path.dirname(_HERE)
 _CSRC = os.path.join(_HERE, "csrc")
 _BUILD = os.path.join(_HERE, "_build")
 LIB_PATH = os.path.join(_BUILD, "libmoe_gb300.so")
-_SOURCES = ["api.cu", "route.cu", "router_tc.cu", "expert_tc.cu", "noalloc.cu", "block.cu"]
-_HEADERS = ["moe_internal.cuh", "tc_ptx.cuh"]
+_SOURCES = ["api.cu", "route.cu", "router_tc.cu", "expert_tc.cu", "noalloc.cu", "block.cu", "ops.cu", "attn.cu"]
+_HEADERS = ["moe_internal.cuh", "tc_ptx.cuh", "ops_internal.cuh"]
+_INCLUDES = ["moe_gb300.h", "moe_ops_gb300.h"]
 NVCC_ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
               "--expt-relaxed-constexpr"]
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_NOT_LOADED = 0, -1, -2, -3
 MOE_ERR_OOM, MOE_ERR_CUDA, MOE_ERR_DEVICE_FLAG = -4, -5, -6
+MOE_DT_BF16, MOE_DT_F16 = 0, 1
+MOE_OPS_ERR_PLAN, MOE_OPS_ERR_INDEX = 32, 64
 
 EXPORTED = ["moe_create", "moe_load_layer", "moe_forward", "moe_forward_host", "moe_destroy", "moe_status_str",
             "moe_get_error", "moe_debug_route", "moe_debug_select", "moe_debug_experts", "moe_profile_stages",
             "moe_profile_stage_name", "moe_profile_begin", "moe_profile_end", "moe_device_bytes", "moe_launch_count",
-            "moe_route_noalloc", "moe_plan", "moe_forward_routed", "moe_debug_pdl_copy"]
+            "moe_route_noalloc", "moe_plan", "moe_forward_routed", "moe_debug_pdl_copy",
+            "moe_add_rmsnorm", "moe_paged_plan", "moe_rotary_append", "moe_attn_create", "moe_attn_forward",
+            "moe_attn_get_error", "moe_attn_device_bytes", "moe_attn_destroy"]
 
 # Revision of each kernel's code; a stored ncu traffic figure is only reported while
 # the revision it was measured on is current. "gateup" and "down" are the decode grouped
@@ -50,7 +55,8 @@ def _nvcc() -> str:
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile the CUDA library in-tree for sm_103a (one -gencode, parallel TUs)."""
     os.makedirs(_BUILD, exist_ok=True)
-    deps = [os.path.join(_CSRC, f) for f in _SOURCES + _HEADERS] + [os.path.join(_ROOT, "include", "moe_gb300.h")]
+    deps = [os.path.join(_CSRC, f) for f in _SOURCES + _HEADERS]
+    deps += [os.path.join(_ROOT, "include", f) for f in _INCLUDES]
     newest = max(os.path.getmtime(d) for d in deps)
     if not force and os.path.exists(LIB_PATH) and os.path.getmtime(LIB_PATH) >= newest:
         return LIB_PATH
@@ -126,6 +132,16 @@ def lib():
         L.moe_launch_count.restype = ctypes.c_int64
         L.moe_launch_count.argtypes = [vp]
         L.moe_route_noalloc.argtypes = [vp, p, p, p, i32, i32, i32, i32, p, p, p, p, p, p, p]
+        packed = ctypes.c_char_p  # argument structs packed by ops.py
+        L.moe_add_rmsnorm.argtypes = [vp, packed]
+        L.moe_paged_plan.argtypes = [vp, packed]
+        L.moe_rotary_append.argtypes = [vp, packed]
+        L.moe_attn_create.argtypes = [ctypes.c_int, ctypes.POINTER(vp)]
+        L.moe_attn_forward.argtypes = [vp, vp, packed]
+        L.moe_attn_get_error.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
+        L.moe_attn_device_bytes.restype = ctypes.c_int64
+        L.moe_attn_device_bytes.argtypes = [vp]
+        L.moe_attn_destroy.argtypes = [vp]
         _lib = L
     return _lib
 
@@ -405,3 +421,16 @@ class MoeLayer:
             self.close()
         except Exception:
             pass
+
+
+_OPS = ("add_rmsnorm", "paged_plan", "rope_frequencies", "rotary_append", "PagedAttention")
+
+
+def __getattr__(name):
+    """The operators beside the layer (ops.py), loaded on first use: importing the package
+    alone needs no PyTorch."""
+    if name in _OPS:
+        from . import ops
+        globals()[name] = getattr(ops, name)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
