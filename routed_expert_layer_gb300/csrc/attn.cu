@@ -1,81 +1,803 @@
-// Attention of new tokens over a paged cache (interface and formula: include/moe_ops_gb300.h).
+// Attention of new tokens over a paged cache (interface and formula: include/moe_ops_gb300.h),
+// on the tensor cores.
 //
-// One warp per (token, query head): an online softmax over the keys the token sees, fp32
-// scores, sums and accumulators. The last visible key bounds the loop, so keys a row does
-// not see are never read.
+//   S = Q K^T (rows: a tile's (token, query head) pairs of one key head; columns: keys)
+//   P = exp2(scale log2(e) (S - m)), l = sum of P, O = P V, out = O / l
+// with m the running row maximum. One pass over the keys; S, P and O live in tensor memory.
+//
+// Rows. The G = Hq / Hkv query heads that share a key head are packed with the tokens: row r
+// of a tile is token r / G, head r % G, TPT = tokens per tile of 128 rows. An item is one
+// (request, key head, QT tiles): all its rows read the same keys.
+//
+// Work. The items, in the order request, key head, tile, lie on one axis on which an item is
+// as long as the keys it reads plus a constant for its start and end. Every CTA takes an
+// equal stretch of the axis, whatever mix of chunk lengths and contexts the call has; an item
+// that crosses a boundary is computed in pieces whose (m, l, O) go through the workspace, and
+// the CTA that finishes an item's last piece joins them in key order (so the result does not
+// depend on which one that was). The axis is laid out from the lengths by every CTA itself.
+//
+// Warps. 0: TMA producer (Q, K and V tiles by page; a page that does not exist is an
+// out-of-range coordinate, which TMA fills with zeros). 1: issues the MMAs. 2, 3: clean V
+// tiles that hold keys some row must not see: rows past the last visible key become zeros,
+// and values that are not finite become zeros and their token is noted, so 0 * inf never
+// reaches a row that does not see them; rows that do see one add it in the end. 4..: softmax,
+// one group of four warps per tile, one thread per row. A row's O is only rescaled when its
+// maximum grew by more than 2^8 since the last rescaling: until then P just exceeds 1, by at
+// most 2^8, which neither the fp32 sums nor P's 16-bit floating point notice.
+//
+// P is rounded to the type of the cache for the second product (the tensor cores take no
+// other); l sums the unrounded values.
+//
+// Two instances per head width. Where every request has at most 128 rows (decoding, a few
+// draft tokens) the call streams the cache: one tile, 64 keys per step, two CTAs per SM, so one
+// CTA's softmax and its items' ends hide behind the other's loads. Longer chunks are bound
+// by the tensor cores and the exponentials: two tiles per CTA, 128 keys per step; the MMAs
+// of one tile run under the softmax of the other, and every K and V tile is used twice.
+#include <algorithm>
+#include <numeric>
+
 #include "ops_internal.cuh"
+#include "tc_ptx.cuh"
 
 struct moe_attn_ctx {
   int device = 0;
   int sm_count = 0;
+  void* mem = nullptr;
+  size_t bytes = 0;
   uint32_t* err = nullptr;
+  int32_t* tickets = nullptr;
+  float* parts = nullptr;
 };
 
 namespace moe {
+
+using namespace ptx;
+
 namespace {
+
+constexpr int kRows = 128;          // rows of a tile (TMEM lanes)
+constexpr int kRuns = 128;          // runs of requests whose cost sums a CTA keeps
+constexpr int kItemCost = 128;      // an item's start and end, in keys
+constexpr int kMinStretch = 256;    // fewer CTAs than this leaves each (in keys) are not worth a join
+constexpr int kNoteSlots = 8;       // pieces whose notes of non-finite tokens are kept (> V stages + 2)
+constexpr float kRescaleLog2 = 8.f;
 
 struct AttnParams {
   moe_attn_args a;
   int p_shift;
+  int G;           // query heads per key head
+  int tpt;         // tokens per tile
+  int box_tok;     // tokens per Q box
   float scale_log2;
   uint32_t* err;
+  int32_t* tickets;  // [CTAs][QT] finished pieces of the split item that starts in the CTA; zero between calls
+  float* parts;      // [2 CTAs][QT] partial results: O [128][D], m [128], l [128]
 };
 
-template <int DT, int D>
-__global__ void __launch_bounds__(128) attn_rows_kernel(const AttnParams p) {
-  constexpr int E = D / 32;
+template <int DT_, int D_, int QT_, int BN_, int NK_, int NV_>
+struct AttnCfg {
+  static constexpr int DT = DT_, D = D_, QT = QT_, BN = BN_, NK = NK_, NV = NV_;
+  static constexpr int kThreads = 128 + 128 * QT;
+  static constexpr int kCtasPerSm = QT == 1 ? 2 : 1;
+  static constexpr int kBlk = BN * 128;          // 64 elements of every key of a tile
+  static constexpr int kTile = D / 64 * kBlk;
+  static constexpr int kQBlk = kRows * 128;
+  static constexpr int kQ = D / 64 * kQBlk;
+  static constexpr size_t kSmem = 1024 + (size_t)QT * kQ + (size_t)(NK + NV) * kTile + kRuns * 8 + 1024;
+  static constexpr uint32_t cols() {
+    uint32_t c = 32;
+    while (c < (uint32_t)(QT * (BN + D))) c <<= 1;
+    return c;
+  }
+  static constexpr uint32_t kCols = cols();
+  static constexpr int kPart = kRows * (D + 2);  // floats of one partial result
+  static_assert(NV + 2 < kNoteSlots, "notes of a piece outlive the pieces that can be loaded behind it");
+};
+
+// One request's share of the axis, and the position of an item on it.
+struct Work {
+  int b, h, i;             // request, key head, tile group
+  int n_new, ctx, q0;      // new tokens, cached tokens before them (negative: rows without keys), first row of q
+  int n_items;             // tile groups
+  int64_t head_cost;       // cost of one key head of the request
+  int64_t base, at, cost;  // axis: start of the head, start and length of the item
+
+  template <int QT>
+  __device__ __forceinline__ bool load(const AttnParams& p, int request) {  // false: rows outside q
+    b = request;
+    const int s = p.a.q_start[b], e = p.a.q_start[b + 1], kv = max(p.a.kv_lens[b], 0);
+    const bool ok = s >= 0 && e <= p.a.N && e >= s;
+    n_new = ok ? e - s : 0;
+    q0 = s;
+    ctx = kv - n_new;
+    const int st = QT * p.tpt;
+    n_items = (n_new + st - 1) / st;
+    const int64_t n = n_items;
+    head_cost = n * (kItemCost + max(ctx, 0)) + st * (n * (n - 1) / 2) + n_new;
+    return ok;
+  }
+  template <int QT>
+  __device__ __forceinline__ void set_item(const AttnParams& p, int64_t before) {
+    at = base + before;
+    cost = kItemCost + max(ctx, 0) + min((i + 1) * QT * p.tpt, n_new);
+  }
+  template <int QT>
+  __device__ void seek(const AttnParams& p, const int64_t* runs, int seg, int64_t x) {
+    int lo = 0, hi = kRuns;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (runs[mid] <= x) lo = mid;
+      else hi = mid;
+    }
+    int64_t acc = runs[lo];
+    int r = lo * seg;
+    load<QT>(p, r);
+    while (x - acc >= (int64_t)p.a.Hkv * head_cost && r + 1 < p.a.B) {
+      acc += (int64_t)p.a.Hkv * head_cost;
+      load<QT>(p, ++r);
+    }
+    h = (int)((x - acc) / head_cost);
+    base = acc + h * head_cost;
+    const int64_t rest = x - base, each = kItemCost + max(ctx, 0), st = QT * p.tpt;
+    lo = 0;
+    hi = n_items;
+    while (hi - lo > 1) {  // the last group that starts at or before rest
+      const int64_t mid = (lo + hi) >> 1;
+      if (mid * each + st * (mid * (mid + 1) / 2) <= rest) lo = (int)mid;
+      else hi = (int)mid;
+    }
+    i = lo;
+    set_item<QT>(p, i * each + st * ((int64_t)i * (i + 1) / 2));
+  }
+  template <int QT>
+  __device__ __forceinline__ void next(const AttnParams& p) {
+    if (i + 1 < n_items) {
+      const int64_t before = at - base + cost;
+      ++i;
+      set_item<QT>(p, before);
+      return;
+    }
+    i = 0;
+    base += head_cost;
+    if (++h == p.a.Hkv) {
+      h = 0;
+      do load<QT>(p, b + 1);
+      while (n_items == 0 && b + 1 < p.a.B);
+    }
+    set_item<QT>(p, 0);
+  }
+};
+
+// The part of an item that falls into a CTA's stretch [x0, x1) of the axis.
+template <int QT, int BN>
+struct Piece {
+  int t0, t1;      // tiles of BN keys
+  int tq1[QT];     // the end for each row tile (its own last visible key)
+  int kv_end;      // keys visible to the item's last row
+  int first_lim;   // keys visible to its first row
+  bool split;
+  __device__ __forceinline__ Piece(const AttnParams& p, const Work& w, int64_t x0, int64_t x1) {
+    const int tok = w.i * QT * p.tpt;
+    kv_end = max(0, w.ctx + min(tok + QT * p.tpt, w.n_new));
+    first_lim = w.ctx + tok + 1;
+    const int nt = (kv_end + BN - 1) / BN;
+    const int64_t lo = max(x0 - w.at, (int64_t)0), hi = min(x1 - w.at, w.cost);
+    split = lo > 0 || hi < w.cost;
+    t0 = (int)min((int64_t)nt, max(lo - kItemCost, (int64_t)0) / BN);
+    t1 = hi == w.cost ? nt : (int)min((int64_t)nt, max(hi - kItemCost, (int64_t)0) / BN);
+#pragma unroll
+    for (int q = 0; q < QT; ++q) {
+      const int end = tok + q * p.tpt < w.n_new ? max(0, w.ctx + min(tok + (q + 1) * p.tpt, w.n_new)) : 0;
+      tq1[q] = min(t1, (end + BN - 1) / BN);
+    }
+  }
+  __device__ __forceinline__ bool tiles() const { return t1 > t0; }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int DT>
+__device__ __forceinline__ bool not_finite(uint32_t half) {  // one 16-bit value
+  constexpr uint32_t e = DT == MOE_DT_BF16 ? 0x7F80u : 0x7C00u;
+  return (half & e) == e;
+}
+
+// mbar_wait by a whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, err));
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
+    attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                const __grid_constant__ CUtensorMap map_v, const __grid_constant__ AttnParams p) {
+  constexpr int D = C::D, QT = C::QT, BN = C::BN, NK = C::NK, NV = C::NV, DT = C::DT;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* sq = smem;
+  uint8_t* sk = sq + QT * C::kQ;
+  uint8_t* sv = sk + NK * C::kTile;
+  int64_t* runs = reinterpret_cast<int64_t*>(sv + NV * C::kTile);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(runs + kRuns);
+  uint64_t *kfull = bar, *kempty = kfull + NK, *vfull = kempty + NK, *vempty = vfull + NV, *vclean = vempty + NV;
+  uint64_t *qfull = vclean + NV, *qempty = qfull + 1, *oempty = qempty + 1, *drain = oempty + 1;
+  uint64_t *sfull = drain + 1, *pfull = sfull + QT, *ofull = pfull + QT, *group = ofull + QT;
+  int64_t* warp_sum = reinterpret_cast<int64_t*>(group + QT);      // [4]
+  uint32_t* notes = reinterpret_cast<uint32_t*>(warp_sum + 4);     // [kNoteSlots][2][8]
+  uint32_t* tmem_slot = notes + kNoteSlots * 16;
+  int* group_flag = reinterpret_cast<int*>(tmem_slot + 1);         // [QT]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NK; ++s) {
+      mbar_init(&kfull[s], 1);
+      mbar_init(&kempty[s], 1);
+    }
+    for (int s = 0; s < NV; ++s) {
+      mbar_init(&vfull[s], 1);
+      mbar_init(&vempty[s], 1);
+      mbar_init(&vclean[s], 2);
+    }
+    mbar_init(qfull, 1);
+    mbar_init(qempty, 1);
+    mbar_init(oempty, 4 * QT);
+    mbar_init(drain, 1);
+    for (int q = 0; q < QT; ++q) {
+      mbar_init(&sfull[q], 1);
+      mbar_init(&pfull[q], 4);
+      mbar_init(&ofull[q], 1);
+      mbar_init(&group[q], 4);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   pdl_entry();
+
+  // the axis: thread t < kRuns sums the costs of a run of requests
+  const int B = p.a.B, seg = (B + kRuns - 1) / kRuns;
+  int64_t mine = 0, upto = 0;
+  if (warp < kRuns / 32) {
+    for (int b = threadIdx.x * seg; b < min(B, (int)(threadIdx.x + 1) * seg); ++b) {
+      Work one;
+      if (!one.load<QT>(p, b) && blockIdx.x == 0) atomicOr(p.err, kErrIndex);
+      mine += (int64_t)p.a.Hkv * one.head_cost;
+    }
+    upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += u;
+    }
+    if (lane == 31) warp_sum[warp] = upto;
+  }
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int k = 0; k < kRuns / 32; ++k) {
+    if (k == warp) runs[threadIdx.x] = total + upto - mine;
+    total += warp_sum[k];
+  }
+  __syncthreads();
+  const int64_t n_ctas = max((int64_t)1, min((int64_t)gridDim.x, total / kMinStretch));
+  int64_t x0 = 0, x1 = 0;
+  if (blockIdx.x < n_ctas) {
+    x0 = total * blockIdx.x / n_ctas;
+    x1 = total * (blockIdx.x + 1) / n_ctas;
+  }
+  Work w{};
+  if (x0 < x1) w.seek<QT>(p, runs, seg, x0);
+  bool more = x0 < x1, ok = true;
+  auto advance = [&] {
+    more = ok && w.at + w.cost < x1;
+    if (more) w.next<QT>(p);
+  };
+
+  if (warp == 0) {
+    // ---- producer: the warp walks together, lanes load and copy one page each ----
+    const int P = p.a.page_size, pages = P >= BN ? 1 : BN / P;
+    const int rows = P >= BN ? BN : P;  // keys per box
+    uint32_t kn = 0, vn = 0, qn = 0;
+    while (more) {
+      const Piece<QT, BN> pc(p, w, x0, x1);
+      if (pc.tiles()) {
+        if (!warp_wait(qempty, (qn & 1) ^ 1u, p.err)) {
+          ok = false;
+          break;
+        }
+        ++qn;
+        if (lane == 0) {
+          const int box_bytes = p.box_tok * p.G * 128;
+          int boxes[QT], n = 0;
+#pragma unroll
+          for (int q = 0; q < QT; ++q) {
+            const int tok = (w.i * QT + q) * p.tpt;
+            boxes[q] = pc.tq1[q] > pc.t0 ? (min(p.tpt, w.n_new - tok) + p.box_tok - 1) / p.box_tok : 0;
+            n += boxes[q];
+          }
+          mbar_arrive_expect_tx(qfull, (uint32_t)(n * (D / 64) * box_bytes));
+          for (int q = 0; q < QT; ++q)
+            for (int x = 0; x < boxes[q]; ++x)
+              for (int d = 0; d < D / 64; ++d)
+                tma_3d(sq + q * C::kQ + d * C::kQBlk + x * box_bytes, &map_q, d * 64, w.h * p.G,
+                       w.q0 + (w.i * QT + q) * p.tpt + x * p.box_tok, qfull);
+        }
+        __syncwarp();
+        const int32_t* table = p.a.block_table + w.b * p.a.table_stride;
+        auto page_of = [&](int t) {  // this lane's page of tile t
+          const int64_t key = (int64_t)t * BN + (int64_t)lane * P;
+          int id = p.a.num_pages;
+          if (lane < pages && key < pc.kv_end) {
+            const int64_t col = key >> p.p_shift;
+            id = col < p.a.W ? table[col] : -1;
+            if (id < 0 || id >= p.a.num_pages) {
+              atomicOr(p.err, kErrIndex);
+              id = p.a.num_pages;
+            }
+          }
+          return id;
+        };
+        int id = page_of(pc.t0);
+        for (int t = pc.t0; t < pc.t1 && ok; ++t) {
+          const int id_next = t + 1 < pc.t1 ? page_of(t + 1) : 0;
+          const int row = P >= BN ? (t * BN) & (P - 1) : 0;
+          const int ks = (int)(kn % NK), vs = (int)(vn % NV);
+          ok = warp_wait(&kempty[ks], ((kn / NK) & 1) ^ 1u, p.err);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&kfull[ks], C::kTile);
+          __syncwarp();
+          if (lane < pages)
+#pragma unroll
+            for (int d = 0; d < D / 64; ++d)
+              tma_4d(sk + ks * C::kTile + d * C::kBlk + lane * rows * 128, &map_k, d * 64, row, w.h, id, &kfull[ks]);
+          ++kn;
+          ok = warp_wait(&vempty[vs], ((vn / NV) & 1) ^ 1u, p.err);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&vfull[vs], C::kTile);
+          __syncwarp();
+          if (lane < pages)
+#pragma unroll
+            for (int d = 0; d < D / 64; ++d)
+              tma_4d(sv + vs * C::kTile + d * C::kBlk + lane * rows * 128, &map_v, d * 64, row, w.h, id, &vfull[vs]);
+          ++vn;
+          id = id_next;
+        }
+      }
+      advance();
+    }
+    if (!ok) {  // copies already issued land before the CTA's shared memory goes away
+      if (qn) warp_wait(qfull, (qn - 1) & 1, p.err);
+      for (uint32_t j = kn > NK ? kn - NK : 0; j < kn; ++j) warp_wait(&kfull[j % NK], (j / NK) & 1, p.err);
+      for (uint32_t j = vn > NV ? vn - NV : 0; j < vn; ++j) warp_wait(&vfull[j % NV], (j / NV) & 1, p.err);
+    }
+  } else if (warp == 1) {
+    // ---- MMA issuer ----
+    if (lane == 0) {
+      constexpr uint32_t kIdS = idesc_16(DT == MOE_DT_BF16, false, kRows, BN);
+      constexpr uint32_t kIdO = idesc_16(DT == MOE_DT_BF16, true, kRows, D);
+      uint32_t kn = 0, vn = 0, pn = 0, on[QT] = {};
+      const uint32_t aq = smem_u32(sq), ak = smem_u32(sk), av = smem_u32(sv);
+      auto issue_s = [&](int q, int ks) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_f16_ss(tmem + q * BN, desc_sw128(aq + q * C::kQ + (kk >> 2) * C::kQBlk + (kk & 3) * 32),
+                     desc_sw128(ak + ks * C::kTile + (kk >> 2) * C::kBlk + (kk & 3) * 32), kIdS, kk > 0);
+        mma_commit(&sfull[q]);
+      };
+      while (more) {
+        const Piece<QT, BN> pc(p, w, x0, x1);
+        if (pc.tiles()) {
+          ok = mbar_wait(qfull, pn & 1, p.err) && mbar_wait(&kfull[kn % NK], (kn / NK) & 1, p.err);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int q = 0; q < QT; ++q)
+            if (pc.t0 < pc.tq1[q]) issue_s(q, (int)(kn % NK));
+          mma_commit(&kempty[kn % NK]);
+          ++kn;
+          if (pc.t0 + 1 == pc.t1) mma_commit(qempty);
+          for (int t = pc.t0; t < pc.t1; ++t) {
+            const int vs = (int)(vn % NV);
+            const bool last = t + 1 == pc.t1;
+            ok = mbar_wait(&vclean[vs], (vn / NV) & 1, p.err);
+            if (ok && !last) ok = mbar_wait(&kfull[kn % NK], (kn / NK) & 1, p.err);
+            if (ok && t == pc.t0) ok = mbar_wait(oempty, (pn & 1) ^ 1u, p.err);
+            if (!ok) break;
+#pragma unroll
+            for (int q = 0; q < QT; ++q) {
+              if (t >= pc.tq1[q]) continue;
+              ok = ok && mbar_wait(&pfull[q], on[q] & 1, p.err);
+              if (!ok) break;
+              ++on[q];
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < BN / 16; ++kk)
+                mma_f16_ts(tmem + QT * BN + q * D, tmem + q * BN + kk * 8,
+                           desc_sw128_mn(av + vs * C::kTile + kk * 2048, C::kBlk), kIdO, t > pc.t0 || kk > 0);
+              if (t + 1 < pc.tq1[q]) issue_s(q, (int)(kn % NK));
+              else mma_commit(&ofull[q]);
+            }
+            if (!ok) break;
+            mma_commit(&vempty[vs]);
+            ++vn;
+            if (!last) {
+              mma_commit(&kempty[kn % NK]);
+              ++kn;
+              if (t + 2 == pc.t1) mma_commit(qempty);
+            }
+          }
+          if (!ok) break;
+          // a row tile without keys in this piece passes it at the MMAs' pace too
+#pragma unroll
+          for (int q = 0; q < QT; ++q)
+            if (pc.tq1[q] <= pc.t0) mma_commit(&ofull[q]);
+          ++pn;
+        }
+        advance();
+      }
+      mma_commit(drain);  // every MMA issued has completed before TMEM is released
+      mbar_wait(drain, 0, p.err);
+    }
+  } else if (warp < 4) {
+    // ---- V tiles that hold keys some row must not see ----
+    const int cw = warp - 2;
+    uint32_t vn = 0, pn = 0;
+    while (more) {
+      const Piece<QT, BN> pc(p, w, x0, x1);
+      if (pc.tiles()) {
+        uint32_t* note = notes + (pn % kNoteSlots) * 16 + cw * 8;
+        if (lane < 8) note[lane] = 0;
+        __syncwarp();
+        for (int t = pc.t0; t < pc.t1; ++t, ++vn) {
+          const int vs = (int)(vn % NV);
+          ok = warp_wait(&vfull[vs], (vn / NV) & 1, p.err);
+          if (!ok) break;
+          if ((int64_t)(t + 1) * BN > pc.first_lim) {
+            for (int c = cw * 32 + lane; c < BN; c += 64) {
+              const int64_t key = (int64_t)t * BN + c;
+              if (key < pc.first_lim) continue;
+              const bool unseen = key >= pc.kv_end;
+              bool odd = false;
+#pragma unroll
+              for (int d = 0; d < D / 64; ++d)
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                  // every lane starts at another 16 bytes of its row: no two share a bank
+                  uint4* u = reinterpret_cast<uint4*>(sv + vs * C::kTile + d * C::kBlk + c * 128 + ((x + lane) & 7) * 16);
+                  if (unseen) {
+                    *u = make_uint4(0, 0, 0, 0);
+                    continue;
+                  }
+                  uint4 val = *u;
+                  uint32_t* word = reinterpret_cast<uint32_t*>(&val);
+                  bool hit = false;
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    if (not_finite<DT>(word[k])) word[k] &= 0xFFFF0000u, hit = true;
+                    if (not_finite<DT>(word[k] >> 16)) word[k] &= 0x0000FFFFu, hit = true;
+                  }
+                  if (hit) *u = val;
+                  odd |= hit;
+                }
+              const int rel = (int)(key - pc.first_lim);  // < QT * tpt <= 256
+              if (odd) atomicOr(&note[rel >> 5], 1u << (rel & 31));
+            }
+            fence_proxy_async();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&vclean[vs]);
+        }
+        if (!ok) break;
+        ++pn;
+      }
+      advance();
+    }
+  } else {
+    // ---- softmax: thread = row r of tile q ----
+    const int q = (warp - 4) >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane, rt = r / p.G, rh = r - rt * p.G;
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const uint32_t ts = tmem + lane_base + q * BN, to = tmem + lane_base + QT * BN + q * D;
+    uint32_t sn = 0, on = 0, pn = 0, gn = 0;
+    const auto group_sync = [&] {  // the tile's four warps
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&group[q]);
+      ok = warp_wait(&group[q], gn++ & 1, p.err) && ok;
+    };
+    while (more) {
+      const Piece<QT, BN> pc(p, w, x0, x1);
+      const int tok = (w.i * QT + q) * p.tpt;           // the tile's first token
+      const int n_tok = min(p.tpt, w.n_new - tok);      // its tokens (<= 0: no such tile)
+      const bool live = rt < n_tok;
+      const bool warp_live = quarter * 32 < n_tok * p.G;
+      const int lim = w.ctx + tok + rt + 1;             // keys this row sees (live rows)
+      const int tile_lim = w.ctx + tok + 1;             // keys every row of the tile sees
+      const int t_end = q == 0 ? pc.tq1[0] : pc.tq1[QT - 1];
+      float m = -INFINITY, l = 0.f;
+      for (int t = pc.t0; t < t_end; ++t) {
+        ok = warp_wait(&sfull[q], sn & 1, p.err);
+        if (!ok) break;
+        ++sn;
+        tc_fence_after();
+        if (warp_live) {
+          uint32_t s[BN];
+#pragma unroll
+          for (int c = 0; c < BN; c += 32) tmem_ld32(ts + c, s + c);
+          tmem_wait_ld();
+          const int64_t key0 = (int64_t)t * BN;
+          if (key0 + BN > tile_lim) {
+            const int see = (int)max(min((int64_t)lim - key0, (int64_t)BN), (int64_t)0);
+#pragma unroll
+            for (int c = 0; c < BN; ++c)
+              if (c >= see) s[c] = 0xFF800000u;
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < BN; c += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(s[c + k])), __uint_as_float(s[c + 4 + k]));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          if (t == pc.t0) {
+            m = top;
+          } else {
+            const bool grow = live && (top - m) * p.scale_log2 > kRescaleLog2;
+            if (__any_sync(0xFFFFFFFFu, grow)) {
+              // S(t) is complete, so is the product of tile t - 1 that was issued before it
+              const float f = grow ? ex2((m - top) * p.scale_log2) : 1.f;
+              if (grow) m = top;
+              l *= f;
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(to + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                tmem_st32(to + c, o);
+                tmem_wait_st();
+              }
+            }
+          }
+          const float off = m == -INFINITY ? 0.f : -m * p.scale_log2;
+          float sum[4] = {};
+#pragma unroll
+          for (int c = 0; c < BN; c += 4) {
+            float e[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              e[k] = ex2(fmaf(__uint_as_float(s[c + k]), p.scale_log2, off));
+              sum[k] += e[k];
+            }
+            s[c / 2] = pack2<DT>(e[0], e[1]);
+            s[c / 2 + 1] = pack2<DT>(e[2], e[3]);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+          for (int c = 0; c < BN / 2; c += 32) tmem_st32(ts + c, s + c);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[q]);
+      }
+      if (!ok) break;
+      // ---- the piece's result: to out, or to the workspace where the item is split ----
+      const bool any = pc.t0 < t_end;
+      if (pc.tiles()) {
+        ok = warp_wait(&ofull[q], on & 1, p.err);
+        if (!ok) break;
+        ++on;
+        tc_fence_after();
+      }
+      int first = 0, pieces = 1;
+      float* part = nullptr;
+      if (pc.split) {
+        const auto owner = [&](int64_t x) { return (int)(((x + 1) * n_ctas - 1) / total); };
+        first = owner(w.at);
+        pieces = owner(w.at + w.cost - 1) - first + 1;
+        part = p.parts + (size_t)((2 * blockIdx.x + (first == (int)blockIdx.x ? 1 : 0)) * QT + q) * C::kPart;
+      }
+      const int64_t n_row = (int64_t)w.q0 + tok + rt;
+      const int head = w.h * p.G + rh;
+      uint16_t* out = (uint16_t*)p.a.out + n_row * p.a.out_tok + (int64_t)head * p.a.out_head;
+      if (warp_live) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const volatile uint32_t* note = notes + (pn % kNoteSlots) * 16;
+        uint32_t noted = 0;
+        if (any && (int64_t)pc.t1 * BN > pc.first_lim)
+#pragma unroll 1
+          for (int k = 0; k < 16; ++k) noted |= note[k];
+        if (any || !pc.split) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            if (any) {
+              __syncwarp();
+              tmem_ld32(to + c, o);
+              tmem_wait_ld();
+            } else {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = 0;
+            }
+            if (noted && live) {  // add what the cleaning took out, where this row sees it
+#pragma unroll 1
+              for (int rel = 0; rel < lim - pc.first_lim; ++rel) {
+                if (!((note[rel >> 5] | note[8 + (rel >> 5)]) >> (rel & 31) & 1)) continue;
+                const int key = pc.first_lim + rel, col = key >> p.p_shift;
+                const int id = p.a.block_table[w.b * p.a.table_stride + col];
+                const uint16_t* v = (const uint16_t*)p.a.v_cache + id * p.a.vc_page +
+                                    (key & (p.a.page_size - 1)) * p.a.vc_row + w.h * p.a.vc_head + c;
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (not_finite<DT>(v[k])) o[k] = __float_as_uint(__uint_as_float(o[k]) + to_f32<DT>(v[k]));
+              }
+            }
+            if (!live) continue;
+            if (pc.split) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 4)
+                *reinterpret_cast<uint4*>(part + r * D + c + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 32; k += 8) {
+                uint4 y;
+                uint32_t* u = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  u[x] = pack2<DT>(__uint_as_float(o[k + 2 * x]) * inv, __uint_as_float(o[k + 2 * x + 1]) * inv);
+                *reinterpret_cast<uint4*>(out + c + k) = y;
+              }
+            }
+          }
+        }
+        if (live) {
+          if (pc.split) {
+            part[kRows * D + r] = m;
+            part[kRows * (D + 1) + r] = l;
+          } else if (p.a.lse) {
+            p.a.lse[n_row * p.a.Hq + head] =
+                l == 0.f ? -INFINITY : (m * p.scale_log2 + log2f(l)) * 0.69314718055994530942f;
+          }
+        }
+      }
+      if (pc.tiles()) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(oempty);
+        ++pn;
+      }
+      if (pc.split && n_tok > 0) {
+        __threadfence();
+        group_sync();
+        if (ok && r == 0) group_flag[q] = atomicAdd(&p.tickets[first * QT + q], 1) == pieces - 1;
+        group_sync();
+        if (!ok) break;
+        const bool join = *(volatile int*)&group_flag[q] != 0;
+        if (join) {
+          __threadfence();
+          if (r == 0) p.tickets[first * QT + q] = 0;
+          // four elements per thread and step; pieces in key order
+          for (int x = r; x < n_tok * p.G * (D / 4); x += kRows) {
+            const int row = x / (D / 4), c = x - row * (D / 4), t = row / p.G;
+            const auto at = [&](int k) {
+              return p.parts + (size_t)((2 * (first + k) + (k == 0 ? 1 : 0)) * QT + q) * C::kPart;
+            };
+            float top = -INFINITY;
+            for (int k = 0; k < pieces; ++k) top = fmaxf(top, __ldcg(at(k) + kRows * D + row));
+            const float base = top == -INFINITY ? 0.f : top;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float sum = 0.f;
+            for (int k = 0; k < pieces; ++k) {
+              const float* pt = at(k);
+              const float lk = __ldcg(pt + kRows * (D + 1) + row);
+              if (lk == 0.f) continue;  // the row saw nothing in this piece; its O may not be written
+              const float f = ex2((__ldcg(pt + kRows * D + row) - base) * p.scale_log2);
+              const float4 o = __ldcg(reinterpret_cast<const float4*>(pt + row * D) + c);
+              sum = fmaf(f, lk, sum);
+              acc.x = fmaf(f, o.x, acc.x);
+              acc.y = fmaf(f, o.y, acc.y);
+              acc.z = fmaf(f, o.z, acc.z);
+              acc.w = fmaf(f, o.w, acc.w);
+            }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const int64_t n = (int64_t)w.q0 + tok + t;
+            const int hd = w.h * p.G + row - t * p.G;
+            *reinterpret_cast<uint2*>((uint16_t*)p.a.out + n * p.a.out_tok + (int64_t)hd * p.a.out_head + 4 * c) =
+                make_uint2(pack2<DT>(acc.x * inv, acc.y * inv), pack2<DT>(acc.z * inv, acc.w * inv));
+            if (p.a.lse && c == 0)
+              p.a.lse[n * p.a.Hq + hd] =
+                  sum == 0.f ? -INFINITY : (base * p.scale_log2 + log2f(sum)) * 0.69314718055994530942f;
+          }
+        }
+      }
+      advance();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc(tmem, C::kCols);
+  }
+}
+
+template <int DT, int D>
+using StreamCfg = AttnCfg<DT, D, 1, 64, 2, 2>;
+template <int DT, int D>
+using ChunkCfg = AttnCfg<DT, D, 2, 128, 3, 2>;
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// A tensor of 16-bit elements read in boxes with 128-byte swizzle; dims innermost first,
+// strides (elements) of the outer dimensions. Host-only, so it may run during stream capture.
+bool make_map(CUtensorMap* map, const void* base, int dt, int rank, const int64_t* dims, const int64_t* strides,
+              const int* box) {
+  static const EncodeTiledFn encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      fn = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(fn);
+  }();
+  if (!encode) return false;
+  cuuint64_t d[4], s[3];
+  cuuint32_t b[4], e[4];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = (cuuint64_t)dims[i];
+    b[i] = (cuuint32_t)box[i];
+    e[i] = 1;
+    // the stride of a dimension of one is never used; TMA still wants a valid one
+    if (i) s[i - 1] = (cuuint64_t)(dims[i] == 1 ? dims[0] : strides[i - 1]) * 2;
+  }
+  return encode(map, dt == MOE_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                (cuuint32_t)rank, const_cast<void*>(base), d, s, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class C>
+cudaError_t attn_configure() {
+  return cudaFuncSetAttribute(attn_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+}
+
+template <class C>
+int attn_launch(const moe_attn_ctx* ctx, const AttnParams& p, cudaStream_t s) {
   const moe_attn_args& a = p.a;
-  const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (item >= (int64_t)a.N * a.Hq) return;
-  const int n = (int)(item / a.Hq), h = (int)(item - (int64_t)n * a.Hq), g = h / (a.Hq / a.Hkv);
-  int lo = 0, hi = a.B;  // the last request that starts at or before n
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.q_start[mid] <= n) lo = mid;
-    else hi = mid;
-  }
-  const int s0 = a.q_start[lo], s1 = a.q_start[lo + 1];
-  if (n < s0 || n >= s1) return;
-  if (s0 < 0 || s1 > a.N) {
-    if (lane == 0) atomicOr(p.err, kErrIndex);
-    return;
-  }
-  const int kv = a.kv_lens[lo];
-  const int64_t seen = (int64_t)kv - (s1 - s0) + (n - s0) + 1;  // keys this row sees
-  const int len = seen < 0 ? 0 : (int)seen;
-  float q[E], o[E] = {};
-  const uint16_t* qp = (const uint16_t*)a.q + n * a.q_tok + h * a.q_head + lane * E;
-#pragma unroll
-  for (int i = 0; i < E; ++i) q[i] = to_f32<DT>(qp[i]);
-  float m = -INFINITY, l = 0.f;
-  bool bad = false;
-  for (int j = 0; j < len; ++j) {
-    const int col = j >> p.p_shift, row = j & (a.page_size - 1);
-    const int page = col < a.W ? a.block_table[lo * a.table_stride + col] : -1;
-    const bool ok = page >= 0 && page < a.num_pages;
-    bad |= !ok;
-    const uint16_t* kp = (const uint16_t*)a.k_cache + page * a.kc_page + row * a.kc_row + g * a.kc_head + lane * E;
-    const uint16_t* vp = (const uint16_t*)a.v_cache + page * a.vc_page + row * a.vc_row + g * a.vc_head + lane * E;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) s = fmaf(q[i], ok ? to_f32<DT>(kp[i]) : 0.f, s);
-#pragma unroll
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    s *= p.scale_log2;
-    const float mn = fmaxf(m, s);
-    const float f = m == -INFINITY ? 0.f : exp2f(m - mn), w = exp2f(s - mn);
-    l = l * f + w;
-#pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = o[i] * f + w * (ok ? to_f32<DT>(vp[i]) : 0.f);
-    m = mn;
-  }
-  if (bad && lane == 0) atomicOr(p.err, kErrIndex);
-  uint16_t* op = (uint16_t*)a.out + n * a.out_tok + h * a.out_head + lane * E;
-#pragma unroll
-  for (int i = 0; i < E; ++i) op[i] = from_f32<DT>(len > 0 ? o[i] / l : 0.f);
-  if (a.lse && lane == 0) a.lse[(int64_t)n * a.Hq + h] = len > 0 ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+  CUtensorMap mq, mk, mv;
+  const int64_t qd[3] = {a.D, a.Hq, a.N}, qs[2] = {a.q_head, a.q_tok};
+  const int qb[3] = {64, p.G, p.box_tok};
+  const int64_t cd[4] = {a.D, a.page_size, a.Hkv, a.num_pages};
+  const int64_t ks[3] = {a.kc_row, a.kc_head, a.kc_page}, vs[3] = {a.vc_row, a.vc_head, a.vc_page};
+  const int cb[4] = {64, a.page_size < C::BN ? a.page_size : C::BN, 1, 1};
+  if (!make_map(&mq, a.q, a.dtype, 3, qd, qs, qb) || !make_map(&mk, a.k_cache, a.dtype, 4, cd, ks, cb) ||
+      !make_map(&mv, a.v_cache, a.dtype, 4, cd, vs, cb))
+    return MOE_ERR_CUDA;
+  return launch_pdl(attn_kernel<C>, dim3((unsigned)(ctx->sm_count * C::kCtasPerSm)), dim3(C::kThreads), C::kSmem, s,
+                    mq, mk, mv, p) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
+}
+
+template <int DT, int D>
+int attn_by_rows(const moe_attn_ctx* ctx, const AttnParams& p, cudaStream_t s) {
+  const int64_t most = p.a.max_new > 0 ? std::min(p.a.max_new, p.a.N) : p.a.N;
+  if (most <= p.tpt) return attn_launch<StreamCfg<DT, D>>(ctx, p, s);
+  return attn_launch<ChunkCfg<DT, D>>(ctx, p, s);
 }
 
 int attn_check(const moe_attn_args* a) {
@@ -93,8 +815,12 @@ int attn_check(const moe_attn_args* a) {
     if (!p || !is_aligned(p, 16)) return MOE_ERR_INVALID_ARG;
   const int64_t strides[] = {a->q_tok,   a->q_head, a->out_tok, a->out_head, a->kc_page,
                              a->kc_row, a->kc_head, a->vc_page, a->vc_row,   a->vc_head};
-  for (int64_t s : strides)
-    if (s < 0 || s % 8 || s >= ((int64_t)1 << 38)) return MOE_ERR_INVALID_ARG;
+  const int64_t extents[] = {a->N, a->Hq, a->N, a->Hq, a->num_pages, a->page_size, a->Hkv, a->num_pages, a->page_size,
+                             a->Hkv};
+  for (int i = 0; i < 10; ++i) {
+    const int64_t s = strides[i];
+    if (s < 0 || s % 8 || s >= ((int64_t)1 << 38) || (s == 0 && extents[i] > 1)) return MOE_ERR_INVALID_ARG;
+  }
   const void* t32[] = {a->block_table, a->q_start, a->kv_lens};
   for (const void* p : t32)
     if (!p || !is_aligned(p, 4)) return MOE_ERR_INVALID_ARG;
@@ -126,13 +852,25 @@ int moe_attn_create(int device, moe_attn_ctx** out) {
   if (!c) return MOE_ERR_OOM;
   c->device = device;
   c->sm_count = prop.multiProcessorCount;
-  if (cudaMalloc(&c->err, 256) != cudaSuccess) {
+  // error word | tickets (one per CTA and row tile) | partial results (two per CTA and row tile)
+  const size_t most = 2 * (size_t)c->sm_count;
+  const size_t head = (256 + most * 4 + 255) / 256 * 256;
+  c->bytes = head + 2 * most * sizeof(float) * AttnCfg<0, 128, 1, 64, 2, 2>::kPart;
+  if (cudaMalloc(&c->mem, c->bytes) != cudaSuccess) {
     cudaGetLastError();
     delete c;
     return MOE_ERR_OOM;
   }
-  if (cudaMemset(c->err, 0, 256) != cudaSuccess) {
-    cudaFree(c->err);
+  c->err = (uint32_t*)c->mem;
+  c->tickets = (int32_t*)((char*)c->mem + 256);
+  c->parts = (float*)((char*)c->mem + head);
+  if (cudaMemset(c->mem, 0, head) != cudaSuccess || attn_configure<StreamCfg<0, 64>>() != cudaSuccess ||
+      attn_configure<StreamCfg<0, 128>>() != cudaSuccess || attn_configure<StreamCfg<1, 64>>() != cudaSuccess ||
+      attn_configure<StreamCfg<1, 128>>() != cudaSuccess || attn_configure<ChunkCfg<0, 64>>() != cudaSuccess ||
+      attn_configure<ChunkCfg<0, 128>>() != cudaSuccess || attn_configure<ChunkCfg<1, 64>>() != cudaSuccess ||
+      attn_configure<ChunkCfg<1, 128>>() != cudaSuccess) {
+    cudaGetLastError();
+    cudaFree(c->mem);
     delete c;
     return MOE_ERR_CUDA;
   }
@@ -150,17 +888,19 @@ int moe_attn_forward(moe_attn_ctx* ctx, void* stream, const moe_attn_args* a) {
   p.p_shift = __builtin_ctz((unsigned)a->page_size);
   p.scale_log2 = a->scale * 1.44269504088896340736f;
   p.err = ctx->err;
-  const dim3 grid((unsigned)(((int64_t)a->N * a->Hq + 3) / 4)), block(128);
+  p.tickets = ctx->tickets;
+  p.parts = ctx->parts;
+  p.G = a->Hq / a->Hkv;
+  // A Q box is a whole number of 8-row swizzle atoms where that fits in a tile, so boxes can be
+  // laid one behind the other; a tile is then a whole number of boxes.
+  p.box_tok = 8 / std::gcd(p.G, 8);
+  if (p.box_tok * p.G > kRows) p.box_tok = kRows / p.G;
+  p.tpt = kRows / (p.box_tok * p.G) * p.box_tok;
   OpsPdl pdl;
   cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e;
   if (a->dtype == MOE_DT_BF16)
-    e = a->D == 64 ? launch_pdl(attn_rows_kernel<MOE_DT_BF16, 64>, grid, block, 0, s, p)
-                   : launch_pdl(attn_rows_kernel<MOE_DT_BF16, 128>, grid, block, 0, s, p);
-  else
-    e = a->D == 64 ? launch_pdl(attn_rows_kernel<MOE_DT_F16, 64>, grid, block, 0, s, p)
-                   : launch_pdl(attn_rows_kernel<MOE_DT_F16, 128>, grid, block, 0, s, p);
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return a->D == 64 ? attn_by_rows<MOE_DT_BF16, 64>(ctx, p, s) : attn_by_rows<MOE_DT_BF16, 128>(ctx, p, s);
+  return a->D == 64 ? attn_by_rows<MOE_DT_F16, 64>(ctx, p, s) : attn_by_rows<MOE_DT_F16, 128>(ctx, p, s);
 }
 
 int moe_attn_get_error(moe_attn_ctx* ctx, uint32_t* bits) {
@@ -174,12 +914,12 @@ int moe_attn_get_error(moe_attn_ctx* ctx, uint32_t* bits) {
   return v ? MOE_ERR_DEVICE_FLAG : MOE_OK;
 }
 
-int64_t moe_attn_device_bytes(const moe_attn_ctx* ctx) { return ctx ? 256 : 0; }
+int64_t moe_attn_device_bytes(const moe_attn_ctx* ctx) { return ctx ? (int64_t)ctx->bytes : 0; }
 
 int moe_attn_destroy(moe_attn_ctx* ctx) {
   if (!ctx) return MOE_OK;
   DeviceGuard g(ctx->device);
-  cudaFree(ctx->err);
+  cudaFree(ctx->mem);
   delete ctx;
   return MOE_OK;
 }
