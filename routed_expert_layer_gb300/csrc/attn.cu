@@ -59,6 +59,7 @@ constexpr int kRows = 128;          // rows of a tile (TMEM lanes)
 constexpr int kRuns = 128;          // runs of requests whose cost sums a CTA keeps
 constexpr int kItemCost = 128;      // an item's start and end, in keys
 constexpr int kMinStretch = 256;    // fewer CTAs than this leaves each (in keys) are not worth a join
+constexpr int kJoin = 4;            // rows a warp joins at once
 constexpr int kNoteSlots = 8;       // pieces whose notes of non-finite tokens are kept (> V stages + 2)
 constexpr float kRescaleLog2 = 8.f;
 
@@ -200,6 +201,53 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 y;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return y;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 y;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
+}
+
+// Keys from `see` on are hidden from this row.
+__device__ __forceinline__ void hide32(uint32_t* v, int see) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k)
+    if (k >= see) v[k] = 0xFF800000u;  // -inf
+}
+__device__ __forceinline__ void max32(const uint32_t* v, float (&mx)[4]) {
+#pragma unroll
+  for (int k = 0; k < 32; k += 2)
+    mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+}
+// 32 scores to weights exp2(s * scale + off), packed to the 16-bit type in v[0..15]; added to sum.
+template <int DT>
+__device__ __forceinline__ void exp32(uint32_t* v, float2 scale, float2 off, float2 (&sum)[2]) {
+#pragma unroll
+  for (int k = 0; k < 32; k += 2) {
+    const float2 x = fma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), scale, off);
+    const float2 e = make_float2(ex2(x.x), ex2(x.y));
+    sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], e);
+    v[k / 2] = pack2<DT>(e.x, e.y);
+  }
+}
+
 template <int DT>
 __device__ __forceinline__ bool not_finite(uint32_t half) {  // one 16-bit value
   constexpr uint32_t e = DT == MOE_DT_BF16 ? 0x7F80u : 0x7C00u;
@@ -225,7 +273,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
   uint64_t* bar = reinterpret_cast<uint64_t*>(runs + kRuns);
   uint64_t *kfull = bar, *kempty = kfull + NK, *vfull = kempty + NK, *vempty = vfull + NV, *vclean = vempty + NV;
   uint64_t *qfull = vclean + NV, *qempty = qfull + 1, *oempty = qempty + 1, *drain = oempty + 1;
-  uint64_t *sfull = drain + 1, *pfull = sfull + QT, *ofull = pfull + QT, *group = ofull + QT;
+  uint64_t *sfull = drain + 1, *pfull = sfull + QT, *ofull = pfull + 2 * QT, *group = ofull + QT;
   int64_t* warp_sum = reinterpret_cast<int64_t*>(group + QT);      // [4]
   uint32_t* notes = reinterpret_cast<uint32_t*>(warp_sum + 4);     // [kNoteSlots][2][8]
   uint32_t* tmem_slot = notes + kNoteSlots * 16;
@@ -248,7 +296,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
     mbar_init(drain, 1);
     for (int q = 0; q < QT; ++q) {
       mbar_init(&sfull[q], 1);
-      mbar_init(&pfull[q], 4);
+      mbar_init(&pfull[2 * q], 4);
+      mbar_init(&pfull[2 * q + 1], 4);
       mbar_init(&ofull[q], 1);
       mbar_init(&group[q], 4);
     }
@@ -269,7 +318,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
   int64_t mine = 0, upto = 0;
   if (warp < kRuns / 32) {
     for (int b = threadIdx.x * seg; b < min(B, (int)(threadIdx.x + 1) * seg); ++b) {
-      Work one;
+      Work one{};
       if (!one.load<QT>(p, b) && blockIdx.x == 0) atomicOr(p.err, kErrIndex);
       mine += (int64_t)p.a.Hkv * one.head_cost;
     }
@@ -382,16 +431,18 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
     }
   } else if (warp == 1) {
     // ---- MMA issuer ----
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t kIdS = idesc_16(DT == MOE_DT_BF16, false, kRows, BN);
       constexpr uint32_t kIdO = idesc_16(DT == MOE_DT_BF16, true, kRows, D);
       uint32_t kn = 0, vn = 0, pn = 0, on[QT] = {};
-      const uint32_t aq = smem_u32(sq), ak = smem_u32(sk), av = smem_u32(sv);
+      // descriptors of the first tiles; the address field (16-byte units) of the others is further on
+      const uint64_t dq = desc_sw128(smem_u32(sq)), dk = desc_sw128(smem_u32(sk));
+      const uint64_t dv = desc_sw128_mn(smem_u32(sv), C::kBlk);
       auto issue_s = [&](int q, int ks) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          mma_f16_ss(tmem + q * BN, desc_sw128(aq + q * C::kQ + (kk >> 2) * C::kQBlk + (kk & 3) * 32),
-                     desc_sw128(ak + ks * C::kTile + (kk >> 2) * C::kBlk + (kk & 3) * 32), kIdS, kk > 0);
+          mma_f16_ss(tmem + q * BN, dq + ((q * C::kQ + (kk >> 2) * C::kQBlk + (kk & 3) * 32) >> 4),
+                     dk + ((ks * C::kTile + (kk >> 2) * C::kBlk + (kk & 3) * 32) >> 4), kIdS, kk > 0);
         mma_commit(&sfull[q]);
       };
       while (more) {
@@ -416,14 +467,21 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
 #pragma unroll
             for (int q = 0; q < QT; ++q) {
               if (t >= pc.tq1[q]) continue;
-              ok = ok && mbar_wait(&pfull[q], on[q] & 1, p.err);
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {  // half of the keys can start while the other is computed
+                ok = ok && mbar_wait(&pfull[2 * q + half], on[q] & 1, p.err);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < BN / 32; ++j) {
+                  const int kk = half * (BN / 32) + j;
+                  mma_f16_ts(tmem + QT * BN + q * D, tmem + q * BN + kk * 8,
+                             dv + ((vs * C::kTile + kk * 2048) >> 4), kIdO,
+                             t > pc.t0 || half > 0 || j > 0);
+                }
+              }
               if (!ok) break;
               ++on[q];
-              tc_fence_after();
-#pragma unroll
-              for (int kk = 0; kk < BN / 16; ++kk)
-                mma_f16_ts(tmem + QT * BN + q * D, tmem + q * BN + kk * 8,
-                           desc_sw128_mn(av + vs * C::kTile + kk * 2048, C::kBlk), kIdO, t > pc.t0 || kk > 0);
               if (t + 1 < pc.tq1[q]) issue_s(q, (int)(kn % NK));
               else mma_commit(&ofull[q]);
             }
@@ -530,24 +588,20 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         ++sn;
         tc_fence_after();
         if (warp_live) {
+          const int64_t key0 = (int64_t)t * BN;
+          const bool masked = key0 + BN > tile_lim;
+          const int see = (int)max(min((int64_t)lim - key0, (int64_t)BN), (int64_t)0);
           uint32_t s[BN];
 #pragma unroll
           for (int c = 0; c < BN; c += 32) tmem_ld32(ts + c, s + c);
-          tmem_wait_ld();
-          const int64_t key0 = (int64_t)t * BN;
-          if (key0 + BN > tile_lim) {
-            const int see = (int)max(min((int64_t)lim - key0, (int64_t)BN), (int64_t)0);
-#pragma unroll
-            for (int c = 0; c < BN; ++c)
-              if (c >= see) s[c] = 0xFF800000u;
-          }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < BN; c += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(s[c + k])), __uint_as_float(s[c + 4 + k]));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          for (int c = 0; c < BN; c += 32) {
+            tmem_wait_ld32(s + c);
+            if (masked) hide32(s + c, see - c);
+            max32(s + c, mx);
+          }
+          const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
           if (t == pc.t0) {
             m = top;
           } else {
@@ -567,29 +621,38 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
                 tmem_st32(to + c, o);
                 tmem_wait_st();
               }
+              // S again, so that its registers need not be kept over the loop above
+#pragma unroll
+              for (int c = 0; c < BN; c += 32) {
+                tmem_ld32(ts + c, s + c);
+                tmem_wait_ld32(s + c);
+                if (masked) hide32(s + c, see - c);
+              }
             }
           }
           const float off = m == -INFINITY ? 0.f : -m * p.scale_log2;
-          float sum[4] = {};
+          const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), off2 = make_float2(off, off);
+          float2 sum[2] = {};
 #pragma unroll
-          for (int c = 0; c < BN; c += 4) {
-            float e[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              e[k] = ex2(fmaf(__uint_as_float(s[c + k]), p.scale_log2, off));
-              sum[k] += e[k];
+          for (int c = 0; c < BN; c += 32) {
+            exp32<DT>(s + c, sc2, off2, sum);
+            tmem_st16(ts + c / 2, s + c);
+            if (c + 32 == BN / 2) {
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&pfull[2 * q]);
             }
-            s[c / 2] = pack2<DT>(e[0], e[1]);
-            s[c / 2 + 1] = pack2<DT>(e[2], e[3]);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-#pragma unroll
-          for (int c = 0; c < BN / 2; c += 32) tmem_st32(ts + c, s + c);
+          sum[0] = add2(sum[0], sum[1]);
+          l += sum[0].x + sum[0].y;
           tmem_wait_st();
+        } else {
+          if (lane == 0) mbar_arrive(&pfull[2 * q]);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[q]);
+        if (lane == 0) mbar_arrive(&pfull[2 * q + 1]);
       }
       if (!ok) break;
       // ---- the piece's result: to out, or to the workspace where the item is split ----
@@ -687,37 +750,54 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         if (join) {
           __threadfence();
           if (r == 0) p.tickets[first * QT + q] = 0;
-          // four elements per thread and step; pieces in key order
-          for (int x = r; x < n_tok * p.G * (D / 4); x += kRows) {
-            const int row = x / (D / 4), c = x - row * (D / 4), t = row / p.G;
-            const auto at = [&](int k) {
-              return p.parts + (size_t)((2 * (first + k) + (k == 0 ? 1 : 0)) * QT + q) * C::kPart;
-            };
-            float top = -INFINITY;
-            for (int k = 0; k < pieces; ++k) top = fmaxf(top, __ldcg(at(k) + kRows * D + row));
-            const float base = top == -INFINITY ? 0.f : top;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            float sum = 0.f;
-            for (int k = 0; k < pieces; ++k) {
-              const float* pt = at(k);
-              const float lk = __ldcg(pt + kRows * (D + 1) + row);
-              if (lk == 0.f) continue;  // the row saw nothing in this piece; its O may not be written
-              const float f = ex2((__ldcg(pt + kRows * D + row) - base) * p.scale_log2);
-              const float4 o = __ldcg(reinterpret_cast<const float4*>(pt + row * D) + c);
-              sum = fmaf(f, lk, sum);
-              acc.x = fmaf(f, o.x, acc.x);
-              acc.y = fmaf(f, o.y, acc.y);
-              acc.z = fmaf(f, o.z, acc.z);
-              acc.w = fmaf(f, o.w, acc.w);
+          // four elements per thread, kJoin rows at once (their loads overlap); pieces in key order
+          const int n_x = n_tok * p.G * (D / 4);
+          for (int x0j = r; x0j < n_x; x0j += kRows * kJoin) {
+            float top[kJoin], sum[kJoin];
+            float4 acc[kJoin];
+#pragma unroll
+            for (int u = 0; u < kJoin; ++u) {
+              top[u] = -INFINITY;
+              sum[u] = 0.f;
+              acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            const int64_t n = (int64_t)w.q0 + tok + t;
-            const int hd = w.h * p.G + row - t * p.G;
-            *reinterpret_cast<uint2*>((uint16_t*)p.a.out + n * p.a.out_tok + (int64_t)hd * p.a.out_head + 4 * c) =
-                make_uint2(pack2<DT>(acc.x * inv, acc.y * inv), pack2<DT>(acc.z * inv, acc.w * inv));
-            if (p.a.lse && c == 0)
-              p.a.lse[n * p.a.Hq + hd] =
-                  sum == 0.f ? -INFINITY : (base * p.scale_log2 + log2f(sum)) * 0.69314718055994530942f;
+            for (int k = 0; k < pieces; ++k) {
+              const float* pt = p.parts + (size_t)((2 * (first + k) + (k == 0 ? 1 : 0)) * QT + q) * C::kPart;
+              float mk[kJoin], lk[kJoin];
+              float4 o[kJoin];
+#pragma unroll
+              for (int u = 0; u < kJoin; ++u) {
+                const int x = min(x0j + u * kRows, n_x - 1), row = x / (D / 4), c = x - row * (D / 4);
+                mk[u] = __ldcg(pt + kRows * D + row);
+                lk[u] = __ldcg(pt + kRows * (D + 1) + row);
+                o[u] = __ldcg(reinterpret_cast<const float4*>(pt + row * D) + c);
+              }
+#pragma unroll
+              for (int u = 0; u < kJoin; ++u) {
+                if (lk[u] == 0.f) continue;  // the row saw nothing in this piece; its O may not be written
+                const float nt = fmaxf(top[u], mk[u]);
+                const float f0 = ex2((top[u] - nt) * p.scale_log2), f = ex2((mk[u] - nt) * p.scale_log2);
+                top[u] = nt;
+                sum[u] = sum[u] * f0 + lk[u] * f;
+                acc[u].x = acc[u].x * f0 + o[u].x * f;
+                acc[u].y = acc[u].y * f0 + o[u].y * f;
+                acc[u].z = acc[u].z * f0 + o[u].z * f;
+                acc[u].w = acc[u].w * f0 + o[u].w * f;
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < kJoin; ++u) {
+              const int x = x0j + u * kRows, row = x / (D / 4), c = x - row * (D / 4), t = row / p.G;
+              if (x >= n_x) continue;
+              const float inv = sum[u] == 0.f ? 0.f : 1.f / sum[u];
+              const int64_t n = (int64_t)w.q0 + tok + t;
+              const int hd = w.h * p.G + row - t * p.G;
+              *reinterpret_cast<uint2*>((uint16_t*)p.a.out + n * p.a.out_tok + (int64_t)hd * p.a.out_head + 4 * c) =
+                  make_uint2(pack2<DT>(acc[u].x * inv, acc[u].y * inv), pack2<DT>(acc[u].z * inv, acc[u].w * inv));
+              if (p.a.lse && c == 0)
+                p.a.lse[n * p.a.Hq + hd] =
+                    sum[u] == 0.f ? -INFINITY : (top[u] * p.scale_log2 + log2f(sum[u])) * 0.69314718055994530942f;
+            }
           }
         }
       }
