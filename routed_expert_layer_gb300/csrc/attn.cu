@@ -84,7 +84,7 @@ struct AttnCfg {
   static constexpr int kTile = D / 64 * kBlk;
   static constexpr int kQBlk = kRows * 128;
   static constexpr int kQ = D / 64 * kQBlk;
-  static constexpr size_t kSmem = 1024 + (size_t)QT * kQ + (size_t)(NK + NV) * kTile + kRuns * 8 + 1024;
+  static constexpr size_t kSmem = 1024 + (size_t)QT * kQ + (size_t)(NK + NV) * kTile + kRuns * 8 + 1024 + 64 * 4 * QT;
   static constexpr uint32_t cols() {
     uint32_t c = 32;
     while (c < (uint32_t)(QT * (BN + D))) c <<= 1;
@@ -225,12 +225,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return y;
 }
 
-// Keys from `see` on are hidden from this row.
-__device__ __forceinline__ void hide32(uint32_t* v, int see) {
-#pragma unroll
-  for (int k = 0; k < 32; ++k)
-    if (k >= see) v[k] = 0xFF800000u;  // -inf
-}
 __device__ __forceinline__ void max32(const uint32_t* v, float (&mx)[4]) {
 #pragma unroll
   for (int k = 0; k < 32; k += 2)
@@ -256,7 +250,7 @@ __device__ __forceinline__ bool not_finite(uint32_t half) {  // one 16-bit value
 
 // mbar_wait by a whole warp, with one answer for all its lanes.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, err));
+  return __all_sync(0xFFFFFFFFu, mbar_wait_suspended(bar, parity, err));
 }
 
 template <class C>
@@ -278,6 +272,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
   uint32_t* notes = reinterpret_cast<uint32_t*>(warp_sum + 4);     // [kNoteSlots][2][8]
   uint32_t* tmem_slot = notes + kNoteSlots * 16;
   int* group_flag = reinterpret_cast<int*>(tmem_slot + 1);         // [QT]
+  // the softmax warps' place on the axis, out of their registers while they work on tiles
+  Work* parked = reinterpret_cast<Work*>(reinterpret_cast<uint8_t*>(bar) + 1024);
+  static_assert(sizeof(Work) <= 64, "space of a parked place");
+  int64_t* axis = warp_sum;  // [4]: total, CTAs in use, x0, x1 (after the sums are taken)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -344,6 +342,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
     x0 = total * blockIdx.x / n_ctas;
     x1 = total * (blockIdx.x + 1) / n_ctas;
   }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    axis[0] = total;
+    axis[1] = n_ctas;
+    axis[2] = x0;
+    axis[3] = x1;
+  }
+  __syncthreads();
   Work w{};
   if (x0 < x1) w.seek<QT>(p, runs, seg, x0);
   bool more = x0 < x1, ok = true;
@@ -438,60 +444,65 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
       // descriptors of the first tiles; the address field (16-byte units) of the others is further on
       const uint64_t dq = desc_sw128(smem_u32(sq)), dk = desc_sw128(smem_u32(sk));
       const uint64_t dv = desc_sw128_mn(smem_u32(sv), C::kBlk);
-      auto issue_s = [&](int q, int ks) {
+      const auto issue_s = [&](int q) {
+        const uint64_t d = dk + ((kn % NK) * C::kTile >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           mma_f16_ss(tmem + q * BN, dq + ((q * C::kQ + (kk >> 2) * C::kQBlk + (kk & 3) * 32) >> 4),
-                     dk + ((ks * C::kTile + (kk >> 2) * C::kBlk + (kk & 3) * 32) >> 4), kIdS, kk > 0);
+                     d + (((kk >> 2) * C::kBlk + (kk & 3) * 32) >> 4), kIdS, kk > 0);
         mma_commit(&sfull[q]);
       };
+      const auto wait_k = [&] { return mbar_wait_suspended(&kfull[kn % NK], (kn / NK) & 1, p.err); };
+      const auto wait_v = [&](uint32_t n) { return mbar_wait_suspended(&vclean[n % NV], (n / NV) & 1, p.err); };
       while (more) {
         const Piece<QT, BN> pc(p, w, x0, x1);
         if (pc.tiles()) {
-          ok = mbar_wait(qfull, pn & 1, p.err) && mbar_wait(&kfull[kn % NK], (kn / NK) & 1, p.err);
+          ok = mbar_wait_suspended(qfull, pn & 1, p.err) && wait_k();
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int q = 0; q < QT; ++q)
-            if (pc.t0 < pc.tq1[q]) issue_s(q, (int)(kn % NK));
+            if (pc.t0 < pc.tq1[q]) issue_s(q);
           mma_commit(&kempty[kn % NK]);
           ++kn;
-          if (pc.t0 + 1 == pc.t1) mma_commit(qempty);
-          for (int t = pc.t0; t < pc.t1; ++t) {
-            const int vs = (int)(vn % NV);
+          const bool one = pc.t0 + 1 == pc.t1;
+          if (one) mma_commit(qempty);
+          ok = wait_v(vn) && (one || wait_k()) && mbar_wait_suspended(oempty, (pn & 1) ^ 1u, p.err);
+          for (int t = pc.t0; t < pc.t1 && ok; ++t) {
             const bool last = t + 1 == pc.t1;
-            ok = mbar_wait(&vclean[vs], (vn / NV) & 1, p.err);
-            if (ok && !last) ok = mbar_wait(&kfull[kn % NK], (kn / NK) & 1, p.err);
-            if (ok && t == pc.t0) ok = mbar_wait(oempty, (pn & 1) ^ 1u, p.err);
-            if (!ok) break;
+            const uint64_t d = dv + ((vn % NV) * C::kTile >> 4);
 #pragma unroll
             for (int q = 0; q < QT; ++q) {
-              if (t >= pc.tq1[q]) continue;
+              if (t < pc.tq1[q]) {
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {  // half of the keys can start while the other is computed
-                ok = ok && mbar_wait(&pfull[2 * q + half], on[q] & 1, p.err);
-                if (!ok) break;
-                tc_fence_after();
+                for (int half = 0; half < 2; ++half) {  // half of the keys can start while the other is computed
+                  ok = ok && mbar_wait_suspended(&pfull[2 * q + half], on[q] & 1, p.err);
+                  if (!ok) break;
+                  tc_fence_after();
 #pragma unroll
-                for (int j = 0; j < BN / 32; ++j) {
-                  const int kk = half * (BN / 32) + j;
-                  mma_f16_ts(tmem + QT * BN + q * D, tmem + q * BN + kk * 8,
-                             dv + ((vs * C::kTile + kk * 2048) >> 4), kIdO,
-                             t > pc.t0 || half > 0 || j > 0);
+                  for (int j = 0; j < BN / 32; ++j) {
+                    const int kk = half * (BN / 32) + j;
+                    mma_f16_ts(tmem + QT * BN + q * D, tmem + q * BN + kk * 8, d + (kk * 2048 >> 4), kIdO,
+                               t > pc.t0 || kk > 0);
+                  }
                 }
+                if (!ok) break;
+                ++on[q];
+                if (t + 1 < pc.tq1[q]) issue_s(q);
+                else mma_commit(&ofull[q]);
               }
-              if (!ok) break;
-              ++on[q];
-              if (t + 1 < pc.tq1[q]) issue_s(q, (int)(kn % NK));
-              else mma_commit(&ofull[q]);
+              if (q + 1 < QT) continue;
+              mma_commit(&vempty[vn % NV]);
+              if (!last) {
+                mma_commit(&kempty[kn % NK]);
+                if (t + 2 == pc.t1) mma_commit(qempty);
+              }
             }
-            if (!ok) break;
-            mma_commit(&vempty[vs]);
             ++vn;
             if (!last) {
-              mma_commit(&kempty[kn % NK]);
               ++kn;
-              if (t + 2 == pc.t1) mma_commit(qempty);
+              ok = ok && wait_v(vn);
+              if (ok && t + 2 < pc.t1) ok = wait_k();
             }
           }
           if (!ok) break;
@@ -504,7 +515,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         advance();
       }
       mma_commit(drain);  // every MMA issued has completed before TMEM is released
-      mbar_wait(drain, 0, p.err);
+      mbar_wait_suspended(drain, 0, p.err);
     }
   } else if (warp < 4) {
     // ---- V tiles that hold keys some row must not see ----
@@ -562,47 +573,71 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
     }
   } else {
     // ---- softmax: thread = row r of tile q ----
+    constexpr int kHalf = BN / 2;
     const int q = (warp - 4) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane, rt = r / p.G, rh = r - rt * p.G;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const uint32_t ts = tmem + lane_base + q * BN, to = tmem + lane_base + QT * BN + q * D;
+    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
     uint32_t sn = 0, on = 0, pn = 0, gn = 0;
-    const auto group_sync = [&] {  // the tile's four warps
+    const auto group_sync = [&] {  // the tile's warps
       __syncwarp();
       if (lane == 0) mbar_arrive(&group[q]);
       ok = warp_wait(&group[q], gn++ & 1, p.err) && ok;
     };
+    Work* const place = reinterpret_cast<Work*>(reinterpret_cast<uint8_t*>(parked) + 64 * (warp - 4));
     while (more) {
-      const Piece<QT, BN> pc(p, w, x0, x1);
-      const int tok = (w.i * QT + q) * p.tpt;           // the tile's first token
-      const int n_tok = min(p.tpt, w.n_new - tok);      // its tokens (<= 0: no such tile)
-      const bool live = rt < n_tok;
-      const bool warp_live = quarter * 32 < n_tok * p.G;
-      const int lim = w.ctx + tok + rt + 1;             // keys this row sees (live rows)
-      const int tile_lim = w.ctx + tok + 1;             // keys every row of the tile sees
-      const int t_end = q == 0 ? pc.tq1[0] : pc.tq1[QT - 1];
+      int t0, t_end, lim, tile_lim;
+      bool live, warp_live;
+      {
+        const Piece<QT, BN> pc(p, w, x0, x1);
+        const int tok = (w.i * QT + q) * p.tpt, n_tok = min(p.tpt, w.n_new - tok);
+        t0 = pc.t0;
+        t_end = q == 0 ? pc.tq1[0] : pc.tq1[QT - 1];
+        live = rt < n_tok;
+        warp_live = quarter * 32 < n_tok * p.G;
+        lim = w.ctx + tok + rt + 1;   // keys this row sees (live rows)
+        tile_lim = w.ctx + tok + 1;   // keys every row of the tile sees
+      }
+      __syncwarp();
+      if (lane == 0) *place = w;
+      __syncwarp();
       float m = -INFINITY, l = 0.f;
-      for (int t = pc.t0; t < t_end; ++t) {
+      for (int t = t0; t < t_end; ++t) {
         ok = warp_wait(&sfull[q], sn & 1, p.err);
         if (!ok) break;
         ++sn;
         tc_fence_after();
         if (warp_live) {
           const int64_t key0 = (int64_t)t * BN;
-          const bool masked = key0 + BN > tile_lim;
-          const int see = (int)max(min((int64_t)lim - key0, (int64_t)BN), (int64_t)0);
-          uint32_t s[BN];
+          if (key0 + BN > tile_lim) {  // hide keys in place: few tiles need it, so it is kept out of the code of the others
+            const int see = (int)max(min((int64_t)lim - key0, (int64_t)BN), (int64_t)0);
+#pragma unroll 1
+            for (int c = 0; c < BN; c += 32) {
+              uint32_t v[32];
+              tmem_ld32(ts + c, v);
+              tmem_wait_ld32(v);
 #pragma unroll
-          for (int c = 0; c < BN; c += 32) tmem_ld32(ts + c, s + c);
+              for (int k = 0; k < 32; ++k)
+                if (c + k >= see) v[k] = 0xFF800000u;  // -inf
+              tmem_st32(ts + c, v);
+            }
+            tmem_wait_st();
+          }
+          uint32_t s[BN];
+          const auto load_s = [&] {
+#pragma unroll
+            for (int c = 0; c < BN; c += 32) tmem_ld32(ts + c, s + c);
+          };
+          load_s();
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int c = 0; c < BN; c += 32) {
             tmem_wait_ld32(s + c);
-            if (masked) hide32(s + c, see - c);
             max32(s + c, mx);
           }
           const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-          if (t == pc.t0) {
+          if (t == t0) {
             m = top;
           } else {
             const bool grow = live && (top - m) * p.scale_log2 > kRescaleLog2;
@@ -615,48 +650,45 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
               for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
                 tmem_ld32(to + c, o);
-                tmem_wait_ld();
+                tmem_wait_ld32(o);
 #pragma unroll
                 for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
                 tmem_st32(to + c, o);
                 tmem_wait_st();
               }
-              // S again, so that its registers need not be kept over the loop above
+              load_s();  // again, so that its registers need not be kept over the loop above
 #pragma unroll
-              for (int c = 0; c < BN; c += 32) {
-                tmem_ld32(ts + c, s + c);
-                tmem_wait_ld32(s + c);
-                if (masked) hide32(s + c, see - c);
-              }
+              for (int c = 0; c < BN; c += 32) tmem_wait_ld32(s + c);
             }
           }
           const float off = m == -INFINITY ? 0.f : -m * p.scale_log2;
-          const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), off2 = make_float2(off, off);
           float2 sum[2] = {};
 #pragma unroll
-          for (int c = 0; c < BN; c += 32) {
-            exp32<DT>(s + c, sc2, off2, sum);
-            tmem_st16(ts + c / 2, s + c);
-            if (c + 32 == BN / 2) {
-              tmem_wait_st();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&pfull[2 * q]);
+          for (int half = 0; half < 2; ++half) {  // the MMAs can start on the first half of the weights
+#pragma unroll
+            for (int c = half * kHalf; c < (half + 1) * kHalf; c += 32) {
+              exp32<DT>(s + c, sc2, make_float2(off, off), sum);
+              tmem_st16(ts + c / 2, s + c);
             }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pfull[2 * q + half]);
           }
           sum[0] = add2(sum[0], sum[1]);
           l += sum[0].x + sum[0].y;
-          tmem_wait_st();
         } else {
           if (lane == 0) mbar_arrive(&pfull[2 * q]);
+          if (lane == 0) mbar_arrive(&pfull[2 * q + 1]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[2 * q + 1]);
       }
       if (!ok) break;
       // ---- the piece's result: to out, or to the workspace where the item is split ----
-      const bool any = pc.t0 < t_end;
+      const bool any = t0 < t_end;
+      w = *place;
+      const Piece<QT, BN> pc(p, w, axis[2], axis[3]);
+      const int tok = (w.i * QT + q) * p.tpt;       // the tile's first token
+      const int n_tok = min(p.tpt, w.n_new - tok);  // its tokens (<= 0: no such tile)
       if (pc.tiles()) {
         ok = warp_wait(&ofull[q], on & 1, p.err);
         if (!ok) break;
@@ -666,7 +698,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
       int first = 0, pieces = 1;
       float* part = nullptr;
       if (pc.split) {
-        const auto owner = [&](int64_t x) { return (int)(((x + 1) * n_ctas - 1) / total); };
+        const auto owner = [&](int64_t x) { return (int)(((x + 1) * axis[1] - 1) / axis[0]); };
         first = owner(w.at);
         pieces = owner(w.at + w.cost - 1) - first + 1;
         part = p.parts + (size_t)((2 * blockIdx.x + (first == (int)blockIdx.x ? 1 : 0)) * QT + q) * C::kPart;
@@ -688,7 +720,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
             if (any) {
               __syncwarp();
               tmem_ld32(to + c, o);
-              tmem_wait_ld();
+              tmem_wait_ld32(o);
             } else {
 #pragma unroll
               for (int k = 0; k < 32; ++k) o[k] = 0;
@@ -801,6 +833,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
           }
         }
       }
+      w = *place;
+      x1 = axis[3];
+      x0 = axis[2];
       advance();
     }
   }
@@ -816,7 +851,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
 template <int DT, int D>
 using StreamCfg = AttnCfg<DT, D, 1, 64, 2, 2>;
 template <int DT, int D>
-using ChunkCfg = AttnCfg<DT, D, 2, 128, 3, 2>;
+using ChunkCfg = AttnCfg<DT, D, 2, 128, 2, 2>;
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -935,7 +970,7 @@ int moe_attn_create(int device, moe_attn_ctx** out) {
   // error word | tickets (one per CTA and row tile) | partial results (two per CTA and row tile)
   const size_t most = 2 * (size_t)c->sm_count;
   const size_t head = (256 + most * 4 + 255) / 256 * 256;
-  c->bytes = head + 2 * most * sizeof(float) * AttnCfg<0, 128, 1, 64, 2, 2>::kPart;
+  c->bytes = head + 2 * most * sizeof(float) * StreamCfg<0, 128>::kPart;
   if (cudaMalloc(&c->mem, c->bytes) != cudaSuccess) {
     cudaGetLastError();
     delete c;
