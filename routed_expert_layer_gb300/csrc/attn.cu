@@ -59,7 +59,6 @@ constexpr int kRows = 128;          // rows of a tile (TMEM lanes)
 constexpr int kRuns = 128;          // runs of requests whose cost sums a CTA keeps
 constexpr int kItemCost = 128;      // an item's start and end, in keys
 constexpr int kMinStretch = 256;    // fewer CTAs than this leaves each (in keys) are not worth a join
-constexpr int kJoin = 4;            // rows a warp joins at once
 constexpr int kNoteSlots = 8;       // pieces whose notes of non-finite tokens are kept (> V stages + 2)
 constexpr float kRescaleLog2 = 8.f;
 
@@ -72,7 +71,7 @@ struct AttnParams {
   float scale_log2;
   uint32_t* err;
   int32_t* tickets;  // [CTAs][QT] finished pieces of the split item that starts in the CTA; zero between calls
-  float* parts;      // [2 CTAs][QT] partial results: O [128][D], m [128], l [128]
+  float* parts;      // [2 CTAs][QT] partial results: O [D/4][128][4], m [128], l [128]
 };
 
 template <int DT_, int D_, int QT_, int BN_, int NK_, int NV_>
@@ -301,6 +300,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
     }
     fence_mbar_init();
   }
+  if (warp == 0 && lane < 3) prefetch_map(lane == 0 ? &map_q : lane == 1 ? &map_k : &map_v);
   if (warp == 1) {
     tmem_alloc(tmem_slot, C::kCols);
     tmem_relinquish();
@@ -705,14 +705,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
       }
       const int64_t n_row = (int64_t)w.q0 + tok + rt;
       const int head = w.h * p.G + rh;
-      uint16_t* out = (uint16_t*)p.a.out + n_row * p.a.out_tok + (int64_t)head * p.a.out_head;
+      const int64_t out_at = n_row * p.a.out_tok + (int64_t)head * p.a.out_head;
       if (warp_live) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const volatile uint32_t* note = notes + (pn % kNoteSlots) * 16;
-        uint32_t noted = 0;
-        if (any && (int64_t)pc.t1 * BN > pc.first_lim)
-#pragma unroll 1
-          for (int k = 0; k < 16; ++k) noted |= note[k];
+        // does any clean warp's note say that a token was not finite?
+        const bool noted = any && (int64_t)pc.t1 * BN > pc.first_lim && __any_sync(0xFFFFFFFFu, lane < 16 && note[lane & 15]);
         if (any || !pc.split) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
@@ -738,21 +736,23 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
                   if (not_finite<DT>(v[k])) o[k] = __float_as_uint(__uint_as_float(o[k]) + to_f32<DT>(v[k]));
               }
             }
-            if (!live) continue;
             if (pc.split) {
+              if (live)
 #pragma unroll
-              for (int k = 0; k < 32; k += 4)
-                *reinterpret_cast<uint4*>(part + r * D + c + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                for (int k = 0; k < 32; k += 4)  // lanes are neighbours
+                  *reinterpret_cast<uint4*>(part + ((c + k) / 4 * kRows + r) * 4) =
+                      make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
             } else {
+              if (live)
 #pragma unroll
-              for (int k = 0; k < 32; k += 8) {
-                uint4 y;
-                uint32_t* u = reinterpret_cast<uint32_t*>(&y);
+                for (int k = 0; k < 32; k += 8) {
+                  uint4 y;
+                  uint32_t* u = reinterpret_cast<uint32_t*>(&y);
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                  u[x] = pack2<DT>(__uint_as_float(o[k + 2 * x]) * inv, __uint_as_float(o[k + 2 * x + 1]) * inv);
-                *reinterpret_cast<uint4*>(out + c + k) = y;
-              }
+                  for (int x = 0; x < 4; ++x)
+                    u[x] = pack2<DT>(__uint_as_float(o[k + 2 * x]) * inv, __uint_as_float(o[k + 2 * x + 1]) * inv);
+                  *reinterpret_cast<uint4*>((uint16_t*)p.a.out + out_at + c + k) = y;
+                }
             }
           }
         }
@@ -782,54 +782,59 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         if (join) {
           __threadfence();
           if (r == 0) p.tickets[first * QT + q] = 0;
-          // four elements per thread, kJoin rows at once (their loads overlap); pieces in key order
-          const int n_x = n_tok * p.G * (D / 4);
-          for (int x0j = r; x0j < n_x; x0j += kRows * kJoin) {
-            float top[kJoin], sum[kJoin];
-            float4 acc[kJoin];
+          // Lane = row, each warp a quarter of the columns, pieces in key order, two at a time (their
+          // loads overlap).
+          constexpr int kCols4 = D / 16;
+          const int rows = n_tok * p.G;
+          for (int r0 = 0; r0 < rows; r0 += 32) {
+            const int row = min(r0 + lane, rows - 1);
+            float top = -INFINITY, sum = 0.f;
+            float4 acc[kCols4];
 #pragma unroll
-            for (int u = 0; u < kJoin; ++u) {
-              top[u] = -INFINITY;
-              sum[u] = 0.f;
-              acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            for (int k = 0; k < pieces; ++k) {
-              const float* pt = p.parts + (size_t)((2 * (first + k) + (k == 0 ? 1 : 0)) * QT + q) * C::kPart;
-              float mk[kJoin], lk[kJoin];
-              float4 o[kJoin];
+            for (int j = 0; j < kCols4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < pieces; k += 2) {
+              float mk[2], lk[2];
+              float4 o[2][kCols4];
 #pragma unroll
-              for (int u = 0; u < kJoin; ++u) {
-                const int x = min(x0j + u * kRows, n_x - 1), row = x / (D / 4), c = x - row * (D / 4);
+              for (int u = 0; u < 2; ++u) {
+                const int kk = min(k + u, pieces - 1);
+                const float* pt = p.parts + (size_t)((2 * (first + kk) + (kk == 0 ? 1 : 0)) * QT + q) * C::kPart;
                 mk[u] = __ldcg(pt + kRows * D + row);
-                lk[u] = __ldcg(pt + kRows * (D + 1) + row);
-                o[u] = __ldcg(reinterpret_cast<const float4*>(pt + row * D) + c);
+                lk[u] = k + u < pieces ? __ldcg(pt + kRows * (D + 1) + row) : 0.f;
+#pragma unroll
+                for (int j = 0; j < kCols4; ++j)
+                  o[u][j] = __ldcg(reinterpret_cast<const float4*>(pt) + (quarter * kCols4 + j) * kRows + row);
               }
 #pragma unroll
-              for (int u = 0; u < kJoin; ++u) {
+              for (int u = 0; u < 2; ++u) {
                 if (lk[u] == 0.f) continue;  // the row saw nothing in this piece; its O may not be written
-                const float nt = fmaxf(top[u], mk[u]);
-                const float f0 = ex2((top[u] - nt) * p.scale_log2), f = ex2((mk[u] - nt) * p.scale_log2);
-                top[u] = nt;
-                sum[u] = sum[u] * f0 + lk[u] * f;
-                acc[u].x = acc[u].x * f0 + o[u].x * f;
-                acc[u].y = acc[u].y * f0 + o[u].y * f;
-                acc[u].z = acc[u].z * f0 + o[u].z * f;
-                acc[u].w = acc[u].w * f0 + o[u].w * f;
+                const float nt = fmaxf(top, mk[u]);
+                const float f0 = ex2((top - nt) * p.scale_log2), f = ex2((mk[u] - nt) * p.scale_log2);
+                top = nt;
+                sum = sum * f0 + lk[u] * f;
+#pragma unroll
+                for (int j = 0; j < kCols4; ++j) {
+                  acc[j].x = acc[j].x * f0 + o[u][j].x * f;
+                  acc[j].y = acc[j].y * f0 + o[u][j].y * f;
+                  acc[j].z = acc[j].z * f0 + o[u][j].z * f;
+                  acc[j].w = acc[j].w * f0 + o[u][j].w * f;
+                }
               }
             }
+            if (r0 + lane >= rows) continue;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const int t = row / p.G, hd = w.h * p.G + row - t * p.G;
+            const int64_t n = (int64_t)w.q0 + tok + t;
+            uint16_t* out = (uint16_t*)p.a.out + n * p.a.out_tok + (int64_t)hd * p.a.out_head + quarter * (D / 4);
 #pragma unroll
-            for (int u = 0; u < kJoin; ++u) {
-              const int x = x0j + u * kRows, row = x / (D / 4), c = x - row * (D / 4), t = row / p.G;
-              if (x >= n_x) continue;
-              const float inv = sum[u] == 0.f ? 0.f : 1.f / sum[u];
-              const int64_t n = (int64_t)w.q0 + tok + t;
-              const int hd = w.h * p.G + row - t * p.G;
-              *reinterpret_cast<uint2*>((uint16_t*)p.a.out + n * p.a.out_tok + (int64_t)hd * p.a.out_head + 4 * c) =
-                  make_uint2(pack2<DT>(acc[u].x * inv, acc[u].y * inv), pack2<DT>(acc[u].z * inv, acc[u].w * inv));
-              if (p.a.lse && c == 0)
-                p.a.lse[n * p.a.Hq + hd] =
-                    sum[u] == 0.f ? -INFINITY : (top[u] * p.scale_log2 + log2f(sum[u])) * 0.69314718055994530942f;
-            }
+            for (int j = 0; j < kCols4; j += 2)
+              *reinterpret_cast<uint4*>(out + 4 * j) =
+                  make_uint4(pack2<DT>(acc[j].x * inv, acc[j].y * inv), pack2<DT>(acc[j].z * inv, acc[j].w * inv),
+                             pack2<DT>(acc[j + 1].x * inv, acc[j + 1].y * inv),
+                             pack2<DT>(acc[j + 1].z * inv, acc[j + 1].w * inv));
+            if (p.a.lse && quarter == 0)
+              p.a.lse[n * p.a.Hq + hd] =
+                  sum == 0.f ? -INFINITY : (top * p.scale_log2 + log2f(sum)) * 0.69314718055994530942f;
           }
         }
       }

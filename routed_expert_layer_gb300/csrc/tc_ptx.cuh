@@ -135,6 +135,11 @@ __device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, int32_
       : "memory");
 }
 
+// Brings a tensor map (a kernel parameter) into the descriptor cache.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // Orders this thread's earlier shared-memory writes before later accesses of the asynchronous
 // proxy (TMA, tcgen05.mma) that another thread issues after synchronising with this one.
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
