@@ -57,8 +57,11 @@ namespace {
 
 constexpr int kRows = 128;          // rows of a tile (TMEM lanes)
 constexpr int kRuns = 128;          // runs of requests whose cost sums a CTA keeps
-constexpr int kItemCost = 128;      // an item's start and end, in keys
-constexpr int kMinStretch = 256;    // fewer CTAs than this leaves each (in keys) are not worth a join
+constexpr int kMinStretch = 256;    // a CTA's least share of the axis (in keys): more CTAs than that are not worth a join
+constexpr int kWhole = 768;         // where a CTA's share is less than twice this, items up to this long are not split
+// What an item's start and end cost, in keys. With one row tile they hide behind the other CTA of the SM.
+template <int QT>
+constexpr int kItemCost = QT == 1 ? 128 : 384;
 constexpr int kNoteSlots = 8;       // pieces whose notes of non-finite tokens are kept (> V stages + 2)
 constexpr float kRescaleLog2 = 8.f;
 
@@ -83,7 +86,7 @@ struct AttnCfg {
   static constexpr int kTile = D / 64 * kBlk;
   static constexpr int kQBlk = kRows * 128;
   static constexpr int kQ = D / 64 * kQBlk;
-  static constexpr size_t kSmem = 1024 + (size_t)QT * kQ + (size_t)(NK + NV) * kTile + kRuns * 8 + 1024 + 64 * 4 * QT;
+  static constexpr size_t kSmem = 1024 + (size_t)QT * kQ + (size_t)(NK + NV) * kTile + kRuns * 8 + 1024 + 64 * 4 * QT + 64;
   static constexpr uint32_t cols() {
     uint32_t c = 32;
     while (c < (uint32_t)(QT * (BN + D))) c <<= 1;
@@ -92,6 +95,23 @@ struct AttnCfg {
   static constexpr uint32_t kCols = cols();
   static constexpr int kPart = kRows * (D + 2);  // floats of one partial result
   static_assert(NV + 2 < kNoteSlots, "notes of a piece outlive the pieces that can be loaded behind it");
+};
+
+// Quotient of non-negative values; the axis usually fits in 32 bits, where a division is several times faster.
+__device__ __forceinline__ int64_t div_floor(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
+// The axis and the calling CTA's stretch [x0, x1) of it: CTA c of n starts at c * (total / n) + min(c, total % n).
+struct Axis {
+  int64_t total, each, x0, x1, whole;
+  int n, extra;
+  __device__ __forceinline__ int64_t start(int c) const { return c * each + min(c, extra); }
+  __device__ __forceinline__ int owner(int64_t x) const {  // the CTA whose stretch holds x
+    const int64_t wide = extra * (each + 1);
+    return (int)(x < wide ? div_floor(x, each + 1) : extra + div_floor(x - wide, each));
+  }
 };
 
 // One request's share of the axis, and the position of an item on it.
@@ -113,22 +133,21 @@ struct Work {
     const int st = QT * p.tpt;
     n_items = (n_new + st - 1) / st;
     const int64_t n = n_items;
-    head_cost = n * (kItemCost + max(ctx, 0)) + st * (n * (n - 1) / 2) + n_new;
+    head_cost = n * (kItemCost<QT> + max(ctx, 0)) + st * (n * (n - 1) / 2) + n_new;
     return ok;
   }
   template <int QT>
   __device__ __forceinline__ void set_item(const AttnParams& p, int64_t before) {
     at = base + before;
-    cost = kItemCost + max(ctx, 0) + min((i + 1) * QT * p.tpt, n_new);
+    cost = kItemCost<QT> + max(ctx, 0) + min((i + 1) * QT * p.tpt, n_new);
   }
+  // The item at x, by a whole warp (every lane gets it).
   template <int QT>
-  __device__ void seek(const AttnParams& p, const int64_t* runs, int seg, int64_t x) {
-    int lo = 0, hi = kRuns;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (runs[mid] <= x) lo = mid;
-      else hi = mid;
-    }
+  __device__ __forceinline__ void seek(const AttnParams& p, const int64_t* runs, int seg, int64_t x) {
+    static_assert(kRuns == 128, "four runs per lane");
+    const int lane = threadIdx.x & 31;
+    int lo = 4 * (__popc(__ballot_sync(0xFFFFFFFFu, runs[4 * lane] <= x)) - 1);  // the last run that starts at or before x
+    lo += __popc(__ballot_sync(0xFFFFFFFFu, runs[lo + (lane & 3)] <= x) & 15) - 1;
     int64_t acc = runs[lo];
     int r = lo * seg;
     load<QT>(p, r);
@@ -136,11 +155,11 @@ struct Work {
       acc += (int64_t)p.a.Hkv * head_cost;
       load<QT>(p, ++r);
     }
-    h = (int)((x - acc) / head_cost);
+    h = (int)div_floor(x - acc, head_cost);
     base = acc + h * head_cost;
-    const int64_t rest = x - base, each = kItemCost + max(ctx, 0), st = QT * p.tpt;
+    const int64_t rest = x - base, each = kItemCost<QT> + max(ctx, 0), st = QT * p.tpt;
+    int hi = n_items;
     lo = 0;
-    hi = n_items;
     while (hi - lo > 1) {  // the last group that starts at or before rest
       const int64_t mid = (lo + hi) >> 1;
       if (mid * each + st * (mid * (mid + 1) / 2) <= rest) lo = (int)mid;
@@ -168,23 +187,30 @@ struct Work {
   }
 };
 
-// The part of an item that falls into a CTA's stretch [x0, x1) of the axis.
+// The part of an item that is a CTA's. A boundary between two stretches counts as the item's start
+// where it lies in the item's first tile or before, and anywhere in an item that is not split.
 template <int QT, int BN>
 struct Piece {
   int t0, t1;      // tiles of BN keys
   int tq1[QT];     // the end for each row tile (its own last visible key)
   int kv_end;      // keys visible to the item's last row
   int first_lim;   // keys visible to its first row
+  int64_t first_part;  // the length of axis in which a boundary counts as the start
+  bool none;       // nothing of the item is this CTA's
   bool split;
-  __device__ __forceinline__ Piece(const AttnParams& p, const Work& w, int64_t x0, int64_t x1) {
+  __device__ __forceinline__ Piece(const AttnParams& p, const Work& w, const Axis& ax) {
     const int tok = w.i * QT * p.tpt;
     kv_end = max(0, w.ctx + min(tok + QT * p.tpt, w.n_new));
     first_lim = w.ctx + tok + 1;
     const int nt = (kv_end + BN - 1) / BN;
-    const int64_t lo = max(x0 - w.at, (int64_t)0), hi = min(x1 - w.at, w.cost);
+    first_part = w.cost <= max(ax.whole, (int64_t)kItemCost<QT> + BN) ? w.cost : kItemCost<QT> + BN;
+    int64_t lo = max(ax.x0 - w.at, (int64_t)0), hi = min(ax.x1 - w.at, w.cost);
+    if (lo < first_part) lo = 0;
+    if (hi < first_part) hi = 0;
+    none = hi == 0;
     split = lo > 0 || hi < w.cost;
-    t0 = (int)min((int64_t)nt, max(lo - kItemCost, (int64_t)0) / BN);
-    t1 = hi == w.cost ? nt : (int)min((int64_t)nt, max(hi - kItemCost, (int64_t)0) / BN);
+    t0 = (int)min((int64_t)nt, max(lo - kItemCost<QT>, (int64_t)0) / BN);
+    t1 = none ? t0 : hi == w.cost ? nt : (int)min((int64_t)nt, max(hi - kItemCost<QT>, (int64_t)0) / BN);
 #pragma unroll
     for (int q = 0; q < QT; ++q) {
       const int end = tok + q * p.tpt < w.n_new ? max(0, w.ctx + min(tok + (q + 1) * p.tpt, w.n_new)) : 0;
@@ -274,7 +300,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
   // the softmax warps' place on the axis, out of their registers while they work on tiles
   Work* parked = reinterpret_cast<Work*>(reinterpret_cast<uint8_t*>(bar) + 1024);
   static_assert(sizeof(Work) <= 64, "space of a parked place");
-  int64_t* axis = warp_sum;  // [4]: total, CTAs in use, x0, x1 (after the sums are taken)
+  Axis* parked_axis = reinterpret_cast<Axis*>(reinterpret_cast<uint8_t*>(parked) + 64 * 4 * QT);
+  static_assert(sizeof(Axis) <= 64, "space of the parked axis");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -336,25 +363,24 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
     total += warp_sum[k];
   }
   __syncthreads();
-  const int64_t n_ctas = max((int64_t)1, min((int64_t)gridDim.x, total / kMinStretch));
-  int64_t x0 = 0, x1 = 0;
-  if (blockIdx.x < n_ctas) {
-    x0 = total * blockIdx.x / n_ctas;
-    x1 = total * (blockIdx.x + 1) / n_ctas;
+  Axis ax;
+  ax.total = total;
+  ax.n = (int)max((int64_t)1, min((int64_t)gridDim.x, total / kMinStretch));
+  ax.each = div_floor(total, ax.n);
+  ax.extra = (int)(total - ax.each * ax.n);
+  ax.whole = ax.each <= 2 * kWhole ? kWhole : 0;
+  ax.x0 = ax.x1 = 0;
+  if (blockIdx.x < ax.n) {
+    ax.x0 = ax.start(blockIdx.x);
+    ax.x1 = ax.start(blockIdx.x + 1);
   }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    axis[0] = total;
-    axis[1] = n_ctas;
-    axis[2] = x0;
-    axis[3] = x1;
-  }
+  if (threadIdx.x == 0) *parked_axis = ax;
   __syncthreads();
   Work w{};
-  if (x0 < x1) w.seek<QT>(p, runs, seg, x0);
-  bool more = x0 < x1, ok = true;
+  if (ax.x0 < ax.x1) w.seek<QT>(p, runs, seg, ax.x0);
+  bool more = ax.x0 < ax.x1, ok = true;
   auto advance = [&] {
-    more = ok && w.at + w.cost < x1;
+    more = ok && w.at + w.cost < ax.x1;
     if (more) w.next<QT>(p);
   };
 
@@ -364,7 +390,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
     const int rows = P >= BN ? BN : P;  // keys per box
     uint32_t kn = 0, vn = 0, qn = 0;
     while (more) {
-      const Piece<QT, BN> pc(p, w, x0, x1);
+      const Piece<QT, BN> pc(p, w, ax);
       if (pc.tiles()) {
         if (!warp_wait(qempty, (qn & 1) ^ 1u, p.err)) {
           ok = false;
@@ -455,7 +481,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
       const auto wait_k = [&] { return mbar_wait_suspended(&kfull[kn % NK], (kn / NK) & 1, p.err); };
       const auto wait_v = [&](uint32_t n) { return mbar_wait_suspended(&vclean[n % NV], (n / NV) & 1, p.err); };
       while (more) {
-        const Piece<QT, BN> pc(p, w, x0, x1);
+        const Piece<QT, BN> pc(p, w, ax);
         if (pc.tiles()) {
           ok = mbar_wait_suspended(qfull, pn & 1, p.err) && wait_k();
           if (!ok) break;
@@ -522,7 +548,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
     const int cw = warp - 2;
     uint32_t vn = 0, pn = 0;
     while (more) {
-      const Piece<QT, BN> pc(p, w, x0, x1);
+      const Piece<QT, BN> pc(p, w, ax);
       if (pc.tiles()) {
         uint32_t* note = notes + (pn % kNoteSlots) * 16 + cw * 8;
         if (lane < 8) note[lane] = 0;
@@ -590,7 +616,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
       int t0, t_end, lim, tile_lim;
       bool live, warp_live;
       {
-        const Piece<QT, BN> pc(p, w, x0, x1);
+        const Piece<QT, BN> pc(p, w, ax);
+        if (pc.none) {
+          advance();
+          continue;
+        }
         const int tok = (w.i * QT + q) * p.tpt, n_tok = min(p.tpt, w.n_new - tok);
         t0 = pc.t0;
         t_end = q == 0 ? pc.tq1[0] : pc.tq1[QT - 1];
@@ -686,7 +716,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
       // ---- the piece's result: to out, or to the workspace where the item is split ----
       const bool any = t0 < t_end;
       w = *place;
-      const Piece<QT, BN> pc(p, w, axis[2], axis[3]);
+      const Piece<QT, BN> pc(p, w, *parked_axis);
       const int tok = (w.i * QT + q) * p.tpt;       // the tile's first token
       const int n_tok = min(p.tpt, w.n_new - tok);  // its tokens (<= 0: no such tile)
       if (pc.tiles()) {
@@ -698,9 +728,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
       int first = 0, pieces = 1;
       float* part = nullptr;
       if (pc.split) {
-        const auto owner = [&](int64_t x) { return (int)(((x + 1) * axis[1] - 1) / axis[0]); };
-        first = owner(w.at);
-        pieces = owner(w.at + w.cost - 1) - first + 1;
+        first = parked_axis->owner(w.at + pc.first_part - 1);
+        pieces = parked_axis->owner(w.at + w.cost - 1) - first + 1;
         part = p.parts + (size_t)((2 * blockIdx.x + (first == (int)blockIdx.x ? 1 : 0)) * QT + q) * C::kPart;
       }
       const int64_t n_row = (int64_t)w.q0 + tok + rt;
@@ -839,8 +868,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         }
       }
       w = *place;
-      x1 = axis[3];
-      x0 = axis[2];
+      ax = *parked_axis;
       advance();
     }
   }
