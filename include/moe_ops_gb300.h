@@ -41,7 +41,7 @@ extern "C" {
  * x, residual, out, residual_out [T][H] with row strides; weight [H] in dtype, or fp32 with
  * weight_f32 = 1. residual_out may be residual itself (in place) and out may be x itself;
  * no other overlap. out or out8 may be NULL (not both); scales goes with out8.
- * residual_out needs residual. 1 <= H <= 32768, T >= 0. */
+ * residual_out needs residual. 1 <= H <= 32768, T >= 0. err: bit 4 = a bounded wait gave up. */
 typedef struct {
   const void* x;
   const void* residual;
@@ -50,6 +50,7 @@ typedef struct {
   void* residual_out;
   uint8_t* out8;
   float* scales;
+  uint32_t* err;
   int64_t x_stride, residual_stride, out_stride, residual_out_stride, out8_stride;
   int32_t T, H, dtype, weight_f32, group;
   float eps;

@@ -1,7 +1,10 @@
 // Operators beside the expert layer whose work is moving data: the residual norm, a serving
 // step's plan, rotary positions with the cache append. Interfaces and formulas:
 // include/moe_ops_gb300.h.
+#include <algorithm>
+
 #include "ops_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace moe {
 
@@ -20,6 +23,7 @@ struct NormParams {
   int64_t x_stride, residual_stride, out_stride, residual_out_stride, out8_stride;
   int T, H, weight_f32, group, n_blocks;
   float eps;
+  uint32_t* err;
 };
 
 template <int DT, int VEC>
@@ -86,56 +90,270 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
   return v;
 }
 
-// One row per block row; thread x holds chunks x, x + blockDim.x, ... of VEC elements in
-// registers, so every input is read once.
-template <int DT, int VEC, int NV>
-__global__ void __launch_bounds__(1024) norm_kernel(const NormParams p) {
+// Three kernels, chosen by width and alignment. All read every input once: a thread holds its chunks of
+// the row in registers between the sum of squares and the outputs. 8 or 9 bytes an element against
+// some 10 operations: bound by memory.
+//
+// norm_staged_kernel (1024 < H <= 14336, 16-byte chunks): blocks stay and walk over the rows, the next
+// rows' bytes come by bulk copies into two stages of shared memory, so the reduction's latency is
+// not added to memory's, and the weights are loaded once per block. At T = 8192, H = 7168, bf16 with
+// residual and 8-bit blocks: 86 us, 6.1 TB/s. Measured on the way: one row per block and register
+// loads with 1, 2, 4, 8 chunks per thread 125, 114, 105, 117 us; walking with the next row's loads in
+// registers 95 us; two blocks per SM with 2, 3, 4 stages 86.1, 87.1, 87.5 us, one block with six 111 us,
+// three blocks of 224 threads 97 us. Single rows too: T = 1 2.4 us a launch in a graph (register loads 2.9).
+// norm_rows_kernel (H <= 1024, 16-byte chunks): several rows per block, one chunk per thread, the next
+// rows' loads issued before this one's reduction; staging rows this short would cost a copy each.
+// norm_any_kernel: one element per chunk, for any width, stride and alignment.
+
+__device__ __forceinline__ uint4 load16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+
+template <int DT>
+__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack2<DT>(u[i]);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+
+// The 8-bit output and scales of a row whose chunks are in t (|t| up to mx in this thread), by the whole block.
+template <int NV>
+__device__ __forceinline__ void write_8bit(const NormParams& p, int64_t row, bool live, const float (&t)[NV][8],
+                                           uint32_t mx, uint32_t* red) {
+  const int tx = threadIdx.x, TX = blockDim.x, H = p.H;
+  if (p.group == 0) {
+    mx = row_max(mx, red);
+    if (live && tx == 0) p.scales[row] = __uint_as_float(mx) / 448.f;
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = (tx + i * TX) * 8;
+    uint32_t m = mx;
+    if (p.group) {  // 16 consecutive threads hold one block of 128 (threads past the row hold zeros)
+      m = 0;
+      if (e < H)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(t[i][j]));
+#pragma unroll
+      for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      if (live && e < H && (tx & 15) == 0) p.scales[row * p.n_blocks + (e >> 7)] = __uint_as_float(m) / 448.f;
+    }
+    if (!live || e >= H) continue;
+    const float s = __uint_as_float(m) / 448.f;
+    const float inv = s > 0.f ? 1.f / s : 1.f;  // zeros stay zeros; a NaN scale keeps its NaN values
+    uint2 q;
+    q.x = e4m3x2(t[i][0] * inv, t[i][1] * inv) | e4m3x2(t[i][2] * inv, t[i][3] * inv) << 16;
+    q.y = e4m3x2(t[i][4] * inv, t[i][5] * inv) | e4m3x2(t[i][6] * inv, t[i][7] * inv) << 16;
+    *reinterpret_cast<uint2*>(p.out8 + row * p.out8_stride + e) = q;
+  }
+}
+
+template <int DT, int NV, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) norm_rows_kernel(const NormParams p) {
+  __shared__ float red_sum[2][32];
+  __shared__ uint32_t red_max[2][32];
+  pdl_entry();
+  const int tx = threadIdx.x, TX = blockDim.x, H = p.H;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int64_t first = (int64_t)blockIdx.x * blockDim.y;
+  uint4 x[NV], r[NV], w[NV];
+  const auto fetch = [&](int64_t at) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = (tx + i * TX) * 8;
+      if (at < p.T && e < H) {
+        x[i] = *reinterpret_cast<const uint4*>(p.x + at * p.x_stride + e);
+        if (p.residual) r[i] = *reinterpret_cast<const uint4*>(p.residual + at * p.residual_stride + e);
+      }
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < NV; ++i) x[i] = r[i] = w[i] = make_uint4(0, 0, 0, 0);
+  fetch(row);
+  if (!p.weight_f32)
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if ((tx + i * TX) * 8 < H) w[i] = load16(reinterpret_cast<const uint16_t*>(p.weight) + (tx + i * TX) * 8);
+  int turn = 0;
+  for (int64_t r0 = first; r0 < p.T; r0 += step, row += step, turn ^= 1) {
+    const bool live = row < p.T;
+    float t[NV][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = (tx + i * TX) * 8;
+      unpack8<DT>(x[i], t[i]);
+      if (p.residual) {
+        float a[8];
+        unpack8<DT>(r[i], a);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[i][j] += a[j];
+        if (p.residual_out && live && e < H) store_vec<DT, 8>(p.residual_out + row * p.residual_out_stride + e, t[i]);
+      }
+      if (live && e < H) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(t[i][j], t[i][j], ss);
+      }
+    }
+    fetch(row + step);
+    const float rs = rsqrtf(row_sum(ss, red_sum[turn]) / (float)H + p.eps);
+    uint32_t mx = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = (tx + i * TX) * 8;
+      float g[8];
+      if (p.weight_f32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = e < H ? __ldg(reinterpret_cast<const float*>(p.weight) + e + j) : 0.f;
+      } else {
+        unpack8<DT>(w[i], g);
+      }
+      const bool in = live && e < H;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        t[i][j] = in ? t[i][j] * rs * g[j] : 0.f;
+        mx = max(mx, abs_bits(t[i][j]));
+      }
+      if (p.out && in) store_vec<DT, 8>(p.out + row * p.out_stride + e, t[i]);
+    }
+    if (p.out8) write_8bit<NV>(p, row, live, t, mx, red_max[turn]);
+  }
+}
+
+constexpr int kNormStages = 2;
+
+// One row per step, NV chunks per thread; thread 0 keeps the next rows' copies in flight. A stage is
+// free for the next copy once the row's reduction has synchronised: every thread has read its part.
+template <int DT, int NV, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) norm_staged_kernel(const NormParams p) {
+  extern __shared__ __align__(128) uint8_t staged[];  // [kNormStages][x row | residual row]
+  __shared__ uint64_t full[kNormStages];
+  __shared__ float red_sum[2][32];
+  __shared__ uint32_t red_max[2][32];
+  const int tx = threadIdx.x, H = p.H, TX = blockDim.x;
+  const uint32_t row_bytes = (uint32_t)H * 2, stage_bytes = p.residual ? 2 * row_bytes : row_bytes;
+  if (tx == 0) {
+    for (int s = 0; s < kNormStages; ++s) ptx::mbar_init(&full[s], 1);
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  pdl_entry();
+  const auto copy = [&](int64_t row, int s) {
+    uint8_t* d = staged + (size_t)s * stage_bytes;
+    ptx::mbar_arrive_expect_tx(&full[s], stage_bytes);
+    ptx::bulk_g2s(d, p.x + row * p.x_stride, row_bytes, &full[s]);
+    if (p.residual) ptx::bulk_g2s(d + row_bytes, p.residual + row * p.residual_stride, row_bytes, &full[s]);
+  };
+  if (tx == 0)
+    for (int s = 0; s < kNormStages; ++s) {
+      const int64_t row = (int64_t)blockIdx.x + (int64_t)s * gridDim.x;
+      if (row < p.T) copy(row, s);
+    }
+  uint4 w[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    w[i] = make_uint4(0, 0, 0, 0);
+    const int e = (tx + i * TX) * 8;
+    if (!p.weight_f32 && e < H) w[i] = load16(reinterpret_cast<const uint16_t*>(p.weight) + e);
+  }
+  uint32_t n = 0;
+  bool ok = true;
+  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, ++n) {
+    const int s = n % kNormStages, turn = n & 1;
+    ok = ptx::mbar_wait_quiet(&full[s], (n / kNormStages) & 1);
+    const uint8_t* d = staged + (size_t)s * stage_bytes;
+    float t[NV][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = tx + i * TX;
+      const bool in = c * 8 < H;
+      unpack8<DT>(in ? *reinterpret_cast<const uint4*>(d + c * 16) : make_uint4(0, 0, 0, 0), t[i]);
+      if (p.residual && in) {
+        float a[8];
+        unpack8<DT>(*reinterpret_cast<const uint4*>(d + row_bytes + c * 16), a);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[i][j] += a[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(t[i][j], t[i][j], ss);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+    if ((tx & 31) == 0) red_sum[turn][tx >> 5] = ss;
+    ok = __syncthreads_and(ok);
+    if (!ok) break;  // a copy did not arrive within the limit
+    if (tx == 0 && row + (int64_t)kNormStages * gridDim.x < p.T) copy(row + (int64_t)kNormStages * gridDim.x, s);
+    ss = 0.f;
+    for (int i = 0; i < TX >> 5; ++i) ss += red_sum[turn][i];
+    const float rs = rsqrtf(ss / (float)H + p.eps);
+    uint32_t mx = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = (tx + i * TX) * 8;
+      if (e >= H) continue;
+      if (p.residual_out) store_vec<DT, 8>(p.residual_out + row * p.residual_out_stride + e, t[i]);
+      float g[8];
+      if (p.weight_f32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = __ldg(reinterpret_cast<const float*>(p.weight) + e + j);
+      } else {
+        unpack8<DT>(w[i], g);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        t[i][j] = t[i][j] * rs * g[j];
+        mx = max(mx, abs_bits(t[i][j]));
+      }
+      if (p.out) store_vec<DT, 8>(p.out + row * p.out_stride + e, t[i]);
+    }
+    if (p.out8) write_8bit<NV>(p, row, true, t, mx, red_max[turn]);
+  }
+  if (!ok && tx == 0) {  // let the copies in flight land before the block's shared memory goes away
+    if (p.err) atomicOr(p.err, ptx::kErrTimeout);
+    for (uint32_t k = n; k < n + kNormStages; ++k)
+      if ((int64_t)blockIdx.x + (int64_t)k * gridDim.x < p.T) ptx::mbar_wait_quiet(&full[k % kNormStages], (k / kNormStages) & 1);
+  }
+}
+
+template <int DT, int NV>
+__global__ void __launch_bounds__(1024) norm_any_kernel(const NormParams p) {
   __shared__ float red_sum[32];
   __shared__ uint32_t red_max[32];
-  extern __shared__ uint32_t block_max[];  // VEC == 1 with blocks of 128: [block rows][n_blocks]
+  extern __shared__ uint32_t block_max[];  // with blocks of 128: [block rows][n_blocks]
   pdl_entry();
   const int tx = threadIdx.x, TX = blockDim.x, H = p.H;
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const bool live = row < p.T;
-  float t[NV][VEC];
+  float t[NV];
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = (tx + i * TX) * VEC;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) t[i][j] = 0.f;
+    const int e = tx + i * TX;
+    t[i] = 0.f;
     if (live && e < H) {
-      load_vec<DT, VEC>(p.x + row * p.x_stride + e, t[i]);
+      t[i] = to_f32<DT>(p.x[row * p.x_stride + e]);
       if (p.residual) {
-        float r[VEC];
-        load_vec<DT, VEC>(p.residual + row * p.residual_stride + e, r);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) t[i][j] += r[j];
-        if (p.residual_out) store_vec<DT, VEC>(p.residual_out + row * p.residual_out_stride + e, t[i]);
+        t[i] += to_f32<DT>(p.residual[row * p.residual_stride + e]);
+        if (p.residual_out) p.residual_out[row * p.residual_out_stride + e] = from_f32<DT>(t[i]);
       }
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) ss = fmaf(t[i][j], t[i][j], ss);
+      ss = fmaf(t[i], t[i], ss);
     }
   }
   const float rs = rsqrtf(row_sum(ss, red_sum) / (float)H + p.eps);
   uint32_t mx = 0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = (tx + i * TX) * VEC;
+    const int e = tx + i * TX;
     if (live && e < H) {
-      float w[VEC];
-      if (p.weight_f32) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) w[j] = reinterpret_cast<const float*>(p.weight)[e + j];
-      } else {
-        load_vec<DT, VEC>(reinterpret_cast<const uint16_t*>(p.weight) + e, w);
-      }
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        t[i][j] = t[i][j] * rs * w[j];
-        mx = max(mx, abs_bits(t[i][j]));
-      }
-      if (p.out) store_vec<DT, VEC>(p.out + row * p.out_stride + e, t[i]);
+      const float w = p.weight_f32 ? reinterpret_cast<const float*>(p.weight)[e]
+                                   : to_f32<DT>(reinterpret_cast<const uint16_t*>(p.weight)[e]);
+      t[i] = t[i] * rs * w;
+      mx = max(mx, abs_bits(t[i]));
+      if (p.out) p.out[row * p.out_stride + e] = from_f32<DT>(t[i]);
     }
   }
   if (!p.out8) return;
@@ -143,66 +361,88 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p) {
   if (p.group == 0) {
     mx = row_max(mx, red_max);
     if (live && tx == 0) p.scales[row] = __uint_as_float(mx) / 448.f;
-  } else if constexpr (VEC == 1) {
+  } else {
     for (int b = tx; b < p.n_blocks; b += TX) bm[b] = 0;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = tx + i * TX;
-      if (live && e < H) atomicMax(&bm[e >> 7], abs_bits(t[i][0]));
+      if (live && e < H) atomicMax(&bm[e >> 7], abs_bits(t[i]));
     }
     __syncthreads();
     for (int b = tx; live && b < p.n_blocks; b += TX) p.scales[row * p.n_blocks + b] = __uint_as_float(bm[b]) / 448.f;
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = (tx + i * TX) * VEC;
-    uint32_t m = mx;
-    if (p.group) {
-      if constexpr (VEC == 1) {
-        m = e < H ? bm[e >> 7] : 0;
-      } else {  // 16 consecutive threads hold one block of 128
-        m = 0;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) m = max(m, abs_bits(t[i][j]));
-#pragma unroll
-        for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        if (live && e < H && (tx & 15) == 0) p.scales[row * p.n_blocks + (e >> 7)] = __uint_as_float(m) / 448.f;
-      }
-    }
+    const int e = tx + i * TX;
     if (!live || e >= H) continue;
-    const float s = __uint_as_float(m) / 448.f;
+    const float s = __uint_as_float(p.group ? bm[e >> 7] : mx) / 448.f;
     const float inv = s > 0.f ? 1.f / s : 1.f;  // zeros stay zeros; a NaN scale keeps its NaN values
-    uint8_t* o = p.out8 + row * p.out8_stride + e;
-    if constexpr (VEC == 8) {
-      uint2 w;
-      w.x = e4m3x2(t[i][0] * inv, t[i][1] * inv) | e4m3x2(t[i][2] * inv, t[i][3] * inv) << 16;
-      w.y = e4m3x2(t[i][4] * inv, t[i][5] * inv) | e4m3x2(t[i][6] * inv, t[i][7] * inv) << 16;
-      *reinterpret_cast<uint2*>(o) = w;
-    } else {
-      *o = (uint8_t)e4m3x2(t[i][0] * inv, 0.f);
-    }
+    p.out8[row * p.out8_stride + e] = (uint8_t)e4m3x2(t[i] * inv, 0.f);
   }
 }
 
-template <int DT, int VEC, int NV>
-cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
-  const int chunks = (p.H + VEC - 1) / VEC;
-  const int tx = ((chunks + NV - 1) / NV + 31) / 32 * 32;
-  const int ry = tx >= 256 ? 1 : 256 / tx;
-  const size_t smem = (VEC == 1 && p.out8 && p.group) ? (size_t)ry * p.n_blocks * 4 : 0;
-  return launch_pdl(norm_kernel<DT, VEC, NV>, dim3((unsigned)((p.T + ry - 1) / ry)), dim3(tx, ry), smem, s, p);
+constexpr int kMaxDevices = 64;
+int current_device() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices ? dev : 0;
+}
+
+// SMs of the current device (a constant of the device, read once for each).
+int sm_count() {
+  static int known[kMaxDevices];
+  const int dev = current_device();
+  if (!known[dev]) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 152;
+    known[dev] = n;
+  }
+  return known[dev];
+}
+
+template <int DT, int NV, int MAXT, int MINB>
+cudaError_t launch_norm_rows(const NormParams& p, cudaStream_t s) {
+  const int tx = ((p.H / 8 + NV - 1) / NV + 31) / 32 * 32;
+  const int ry = std::max(1, 128 / tx);
+  const int64_t blocks = ((int64_t)p.T + ry - 1) / ry;
+  const int64_t resident = (int64_t)sm_count() * MINB * (MAXT / (tx * ry));
+  return launch_pdl(norm_rows_kernel<DT, NV, MAXT, MINB>, dim3((unsigned)std::min(blocks, resident)), dim3(tx, ry), 0, s, p);
+}
+
+template <int DT, int NV, int MAXT, int MINB>
+cudaError_t launch_norm_staged(const NormParams& p, cudaStream_t s) {
+  const int tx = ((p.H / 8 + NV - 1) / NV + 31) / 32 * 32;
+  const size_t smem = (size_t)kNormStages * p.H * (p.residual ? 4 : 2);
+  static bool configured[kMaxDevices];  // the opt-in lasts for the process
+  const int dev = current_device();
+  if (!configured[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(norm_staged_kernel<DT, NV, MAXT, MINB>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kNormStages * MAXT * NV * 32);
+    if (e != cudaSuccess) return e;
+    configured[dev] = true;
+  }
+  const int per_sm = std::max(1, std::min(MINB * (MAXT / tx), (int)(233472 / (smem + 1024 + 768))));
+  return launch_pdl(norm_staged_kernel<DT, NV, MAXT, MINB>, dim3((unsigned)std::min<int64_t>(p.T, (int64_t)sm_count() * per_sm)),
+                    dim3(tx), smem, s, p);
+}
+
+template <int DT, int NV>
+cudaError_t launch_norm_any(const NormParams& p, cudaStream_t s) {
+  const int tx = ((p.H + NV - 1) / NV + 31) / 32 * 32;
+  const int ry = std::max(1, 256 / tx);
+  const size_t smem = p.out8 && p.group ? (size_t)ry * p.n_blocks * 4 : 0;
+  return launch_pdl(norm_any_kernel<DT, NV>, dim3((unsigned)((p.T + ry - 1) / ry)), dim3(tx, ry), smem, s, p);
 }
 
 template <int DT>
 cudaError_t norm_by_size(const NormParams& p, bool vec, cudaStream_t s) {
   if (vec) {
-    if (p.H <= 8 * 1024) return launch_norm<DT, 8, 1>(p, s);
-    if (p.H <= 16 * 1024) return launch_norm<DT, 8, 2>(p, s);
-    return launch_norm<DT, 8, 4>(p, s);
+    if (p.H <= 1024) return launch_norm_rows<DT, 1, 128, 8>(p, s);
+    if (p.H <= 8192) return launch_norm_staged<DT, 2, 512, 2>(p, s);
+    if (p.H <= 14336) return launch_norm_staged<DT, 2, 896, 1>(p, s);
   }
-  if (p.H <= 4 * 1024) return launch_norm<DT, 1, 4>(p, s);
-  return launch_norm<DT, 1, 32>(p, s);
+  if (p.H <= 4 * 1024) return launch_norm_any<DT, 4>(p, s);
+  return launch_norm_any<DT, 32>(p, s);
 }
 
 // ---- a serving step's plan ---------------------------------------------------------------------
@@ -327,104 +567,164 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const moe_paged_plan
 
 constexpr int kRotaryThreads = 256;
 
-// VEC: 1 = one pair (or element) per item; 8 = 16-byte vectors.
-template <int DT, int VEC, bool INTER>
-__global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const moe_rotary_args a, int p_shift) {
-  __shared__ float2 cs[512];
+// A rotary pair's turns per position as a 64-bit fraction of a turn: position * fraction mod 2^64 is the
+// angle's, exactly, and costs an integer product (a 32-bit float angle would be off by 2^-24 of itself:
+// a hundredth of a radian at position 10^5).
+__device__ __forceinline__ uint64_t turn_fraction(double inv_freq) {
+  double t = inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
+  t -= floor(t);
+  return __double2ull_rn(t * 18446744073709551616.0);
+}
+__device__ __forceinline__ float2 turned(uint64_t fraction, int pos, float mscale) {
+  const int32_t top = (int32_t)(((uint64_t)(int64_t)pos * fraction) >> 32);  // signed fraction of a turn
+  float sn, cn;
+  sincospif((float)top * (1.f / 2147483648.f), &sn, &cn);
+  return make_float2(cn * mscale, sn * mscale);
+}
+
+// Where a token's k and v go: false if nowhere (slot -1, or outside the cache, which is reported).
+__device__ __forceinline__ bool cache_row(const moe_rotary_args& a, int p_shift, int slot, int64_t& kc, int64_t& vc) {
+  const bool ok = slot >= 0 && slot < (a.num_pages << p_shift);
+  if (slot < -1 || (slot >= 0 && !ok)) {
+    if (threadIdx.x == 0 && blockIdx.y == 0 && a.err) atomicOr(a.err, kErrIndex);
+  }
+  const int64_t page = slot >> p_shift, row = slot & (a.page_size - 1);
+  kc = page * a.kc_page + row * a.kc_row;
+  vc = page * a.vc_page + row * a.vc_row;
+  return ok;
+}
+
+// 16-byte pieces. A token's work is the same list of items for every token: a rotated piece (in the half
+// layout with its partner half a rotary width away), a piece that passes, a piece of v. A thread
+// works out its U items once and then walks over tokens: all its loads first, then the token's
+// cosines and sines (shared by the heads; one exchange per token), then the products and stores.
+// Every element is read and written once, so memory bounds it: N = 8192, 96 + 2 x 8 heads of 128, bf16:
+// 72.0 us, 6.5 TB/s. U items per thread and blocks per SM measured there: 4 and 3 72.0, 4 and 4 (spills)
+// 87.5, 2 and 4 78.0, 2 and 6 77.4, 1 and 8 77.4 us; one item after another with two barriers per token 84 us.
+template <int DT, bool INTER, int U, int MINB>
+__global__ void __launch_bounds__(kRotaryThreads, MINB) rotary_kernel(const moe_rotary_args a, int p_shift) {
+  // pair i sits at i + i / 8 * 2: pieces of 8 pairs are 80 bytes apart, so lanes on different pieces do not
+  // meet in a bank
+  __shared__ __align__(16) float2 cs[2][512 + 128];
   pdl_entry();
-  const int half = a.rot / 2;
-  // Angle in turns as a 64-bit fraction: pos * (inv_freq / 2 pi) mod 1 is an integer product.
-  auto fraction = [&](int i) -> uint64_t {
-    double t = a.inv_freq[i] * 0.15915494309189533577;
-    t -= floor(t);
-    return __double2ull_rn(t * 18446744073709551616.0);
-  };
-  uint64_t f0 = threadIdx.x < half ? fraction(threadIdx.x) : 0;
-  const int n_slots = a.num_pages << p_shift;
-  // items of a token: rotated heads (q then k) in pieces, then v heads in pieces
-  const int r_pieces = INTER || VEC == 1 ? (VEC == 1 ? half : a.rot / 8) : half / 8;
-  const int c_pieces = (a.D - a.rot) / (VEC == 1 ? 1 : 8);  // unrotated rest of a head
-  const int v_pieces = a.D / (VEC == 1 ? 1 : 8);
-  const int h_pieces = r_pieces + c_pieces;
-  const int heads = a.Hq + a.Hkv;
-  const int n_items = heads * h_pieces + a.Hkv * v_pieces;
-  for (int n = blockIdx.x; n < a.N; n += gridDim.x) {
-    const int pos = a.positions[n];
-    for (int i = threadIdx.x; i < half; i += kRotaryThreads) {
-      const uint64_t f = i == (int)threadIdx.x ? f0 : fraction(i);
-      const int32_t top = (int32_t)(((uint64_t)(int64_t)pos * f) >> 32);  // signed fraction of a turn
-      float sn, cn;
-      sincospif((float)top * (1.f / 2147483648.f), &sn, &cn);
-      cs[i] = make_float2(cn * a.mscale, sn * a.mscale);
+  const int tid = threadIdx.x, half = a.rot / 2;
+  const int r_pieces = INTER ? a.rot / 8 : half / 8, c_pieces = (a.D - a.rot) / 8, v_pieces = a.D / 8;
+  const int h_pieces = r_pieces + c_pieces, heads = a.Hq + a.Hkv, n_rot = heads * h_pieces;
+  int64_t from[U], to[U];
+  int kind[U], pair[U];  // kind: 0 nothing, 1 q, 2 k, 3 v; pair: the piece's first rotary pair, or -1
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int it = ((int)blockIdx.y * U + u) * kRotaryThreads + tid;
+    kind[u] = 0;
+    pair[u] = -1;
+    from[u] = to[u] = 0;
+    if (it < n_rot) {
+      const int h = it / h_pieces;
+      int piece = it - h * h_pieces, at = piece * 8;
+      if (piece < r_pieces) pair[u] = INTER ? piece * 4 : piece * 8;
+      else at = a.rot + (piece - r_pieces) * 8;
+      kind[u] = h < a.Hq ? 1 : 2;
+      from[u] = (h < a.Hq ? h * a.q_head : (h - a.Hq) * a.k_head) + at;
+      to[u] = (h < a.Hq ? h * a.qo_head : (h - a.Hq) * a.kc_head) + at;
+    } else if (it < n_rot + a.Hkv * v_pieces) {
+      const int j = it - n_rot, h = j / v_pieces, at = (j - h * v_pieces) * 8;
+      kind[u] = 3;
+      from[u] = h * a.v_head + at;
+      to[u] = h * a.vc_head + at;
     }
-    const int slot = a.slots[n];
-    const bool append = slot >= 0 && slot < n_slots;
-    if ((slot < -1 || slot >= n_slots) && threadIdx.x == 0 && blockIdx.y == 0 && a.err) atomicOr(a.err, kErrIndex);
-    const int64_t page = append ? slot >> p_shift : 0, prow = append ? slot & (a.page_size - 1) : 0;
-    const uint16_t* q = (const uint16_t*)a.q + n * a.q_tok;
-    const uint16_t* k = (const uint16_t*)a.k + n * a.k_tok;
-    const uint16_t* v = (const uint16_t*)a.v + n * a.v_tok;
-    uint16_t* qo = (uint16_t*)a.q_out + n * a.qo_tok;
-    uint16_t* kc = (uint16_t*)a.k_cache + page * a.kc_page + prow * a.kc_row;
-    uint16_t* vc = (uint16_t*)a.v_cache + page * a.vc_page + prow * a.vc_row;
-    __syncthreads();
-    for (int it = blockIdx.y * kRotaryThreads + threadIdx.x; it < n_items; it += gridDim.y * kRotaryThreads) {
-      const uint16_t* src;
-      uint16_t* dst;
-      int piece;
-      bool rotated = false, write = true;
-      if (it < heads * h_pieces) {
-        const int h = it / h_pieces;
-        piece = it - h * h_pieces;
-        if (h < a.Hq) {
-          src = q + h * a.q_head;
-          dst = qo + h * a.qo_head;
-        } else {
-          src = k + (h - a.Hq) * a.k_head;
-          dst = kc + (h - a.Hq) * a.kc_head;
-          write = append;
-        }
-        rotated = piece < r_pieces;
-        if (!rotated) {
-          src += a.rot;
-          dst += a.rot;
-          piece -= r_pieces;
-        }
-      } else {
-        const int j = it - heads * h_pieces, h = j / v_pieces;
-        piece = j - h * v_pieces;
-        src = v + h * a.v_head;
-        dst = vc + h * a.vc_head;
-        write = append;
+  }
+  const uint64_t f0 = tid < half ? turn_fraction(a.inv_freq[tid]) : 0;
+  int turn = 0;
+  for (int n = blockIdx.x; n < a.N; n += gridDim.x, turn ^= 1) {
+    int64_t kc, vc;
+    const bool append = cache_row(a, p_shift, a.slots[n], kc, vc);
+    const int pos = a.positions[n];
+    uint4 x[U], z[INTER ? 1 : U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (kind[u] == 0 || (kind[u] > 1 && !append)) continue;
+      const uint16_t* src = (kind[u] == 1   ? (const uint16_t*)a.q + n * a.q_tok
+                             : kind[u] == 2 ? (const uint16_t*)a.k + n * a.k_tok
+                                            : (const uint16_t*)a.v + n * a.v_tok) + from[u];
+      x[u] = *reinterpret_cast<const uint4*>(src);
+      if constexpr (!INTER)
+        if (pair[u] >= 0) z[u] = *reinterpret_cast<const uint4*>(src + half);
+    }
+    for (int i = tid; i < half; i += kRotaryThreads)
+      cs[turn][i + (i >> 3) * 2] = turned(i == tid ? f0 : turn_fraction(a.inv_freq[i]), pos, a.mscale);
+    __syncthreads();  // one per token: the next token's values go to the other buffer
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (kind[u] == 0 || (kind[u] > 1 && !append)) continue;
+      uint16_t* dst = (kind[u] == 1   ? (uint16_t*)a.q_out + n * a.qo_tok
+                       : kind[u] == 2 ? (uint16_t*)a.k_cache + kc
+                                      : (uint16_t*)a.v_cache + vc) + to[u];
+      if (pair[u] < 0) {
+        *reinterpret_cast<uint4*>(dst) = x[u];
+        continue;
       }
-      if (!write) continue;
-      if (!rotated) {
-        if constexpr (VEC == 8)
-          *reinterpret_cast<uint4*>(dst + piece * 8) = *reinterpret_cast<const uint4*>(src + piece * 8);
-        else
-          dst[piece] = src[piece];
-      } else if constexpr (VEC == 8 && INTER) {
-        float x[8], y[8];
-        load_vec<DT, 8>(src + piece * 8, x);
+      const float2* c = cs[turn] + pair[u] + (pair[u] >> 3) * 2;
+      float p[8], y[8];
+      unpack8<DT>(x[u], p);
+      if constexpr (INTER) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 c = cs[piece * 4 + j];
-          y[2 * j] = x[2 * j] * c.x - x[2 * j + 1] * c.y;
-          y[2 * j + 1] = x[2 * j] * c.y + x[2 * j + 1] * c.x;
+          y[2 * j] = p[2 * j] * c[j].x - p[2 * j + 1] * c[j].y;
+          y[2 * j + 1] = p[2 * j] * c[j].y + p[2 * j + 1] * c[j].x;
         }
-        store_vec<DT, 8>(dst + piece * 8, y);
-      } else if constexpr (VEC == 8) {
-        float x[8], z[8], y[8], w[8];
-        load_vec<DT, 8>(src + piece * 8, x);
-        load_vec<DT, 8>(src + half + piece * 8, z);
+      } else {
+        float q[8], w[8];
+        unpack8<DT>(z[u], q);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float2 c = cs[piece * 8 + j];
-          y[j] = x[j] * c.x - z[j] * c.y;
-          w[j] = x[j] * c.y + z[j] * c.x;
+          y[j] = p[j] * c[j].x - q[j] * c[j].y;
+          w[j] = p[j] * c[j].y + q[j] * c[j].x;
         }
-        store_vec<DT, 8>(dst + piece * 8, y);
-        store_vec<DT, 8>(dst + half + piece * 8, w);
+        store_vec<DT, 8>(dst + half, w);
+      }
+      store_vec<DT, 8>(dst, y);
+    }
+  }
+}
+
+// One pair or element per item: any rotary width, stride and alignment.
+template <int DT, bool INTER>
+__global__ void __launch_bounds__(kRotaryThreads) rotary_any_kernel(const moe_rotary_args a, int p_shift) {
+  __shared__ float2 cs[512];
+  pdl_entry();
+  const int half = a.rot / 2, heads = a.Hq + a.Hkv, per_head = half + a.D - a.rot;
+  const int n_items = heads * per_head + a.Hkv * a.D;
+  for (int n = blockIdx.x; n < a.N; n += gridDim.x) {
+    for (int i = threadIdx.x; i < half; i += kRotaryThreads)
+      cs[i] = turned(turn_fraction(a.inv_freq[i]), a.positions[n], a.mscale);
+    int64_t kc, vc;
+    const bool append = cache_row(a, p_shift, a.slots[n], kc, vc);
+    __syncthreads();
+    for (int it = threadIdx.x; it < n_items; it += kRotaryThreads) {
+      const uint16_t* src;
+      uint16_t* dst;
+      int piece, h;
+      bool rotated = false;
+      if (it < heads * per_head) {
+        h = it / per_head;
+        piece = it - h * per_head;
+        rotated = piece < half;
+        if (!rotated) piece += a.rot - half;
+        src = h < a.Hq ? (const uint16_t*)a.q + n * a.q_tok + h * a.q_head
+                       : (const uint16_t*)a.k + n * a.k_tok + (h - a.Hq) * a.k_head;
+        dst = h < a.Hq ? (uint16_t*)a.q_out + n * a.qo_tok + h * a.qo_head
+                       : (uint16_t*)a.k_cache + kc + (h - a.Hq) * a.kc_head;
+        if (h >= a.Hq && !append) continue;
+      } else {
+        if (!append) continue;
+        const int j = it - heads * per_head;
+        h = j / a.D;
+        piece = j - h * a.D;
+        src = (const uint16_t*)a.v + n * a.v_tok + h * a.v_head;
+        dst = (uint16_t*)a.v_cache + vc + h * a.vc_head;
+      }
+      if (!rotated) {
+        dst[piece] = src[piece];
       } else {
         const int i0 = INTER ? 2 * piece : piece, i1 = INTER ? 2 * piece + 1 : piece + half;
         const float x = to_f32<DT>(src[i0]), z = to_f32<DT>(src[i1]);
@@ -437,14 +737,23 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const moe_rotary
   }
 }
 
-template <int DT>
+template <int DT, bool INTER, int U, int MINB>
+cudaError_t launch_rotary_vec(const moe_rotary_args& a, int groups, int p_shift, cudaStream_t s) {
+  const int y = (groups + U - 1) / U;
+  const int x = std::max(1, std::min(a.N, MINB * sm_count() / y));
+  return launch_pdl(rotary_kernel<DT, INTER, U, MINB>, dim3((unsigned)x, (unsigned)y), dim3(kRotaryThreads), 0, s, a, p_shift);
+}
+
+template <int DT, bool INTER>
 cudaError_t launch_rotary(const moe_rotary_args& a, bool vec, int p_shift, cudaStream_t s) {
-  const dim3 grid((unsigned)min(a.N, 65535)), block(kRotaryThreads);
-  if (vec)
-    return a.interleaved ? launch_pdl(rotary_kernel<DT, 8, true>, grid, block, 0, s, a, p_shift)
-                         : launch_pdl(rotary_kernel<DT, 8, false>, grid, block, 0, s, a, p_shift);
-  return a.interleaved ? launch_pdl(rotary_kernel<DT, 1, true>, grid, block, 0, s, a, p_shift)
-                       : launch_pdl(rotary_kernel<DT, 1, false>, grid, block, 0, s, a, p_shift);
+  if (!vec)
+    return launch_pdl(rotary_any_kernel<DT, INTER>, dim3((unsigned)std::min(a.N, 65535)), dim3(kRotaryThreads), 0, s, a,
+                      p_shift);
+  const int64_t items = (int64_t)(a.Hq + a.Hkv) * ((INTER ? a.rot : a.rot / 2) + a.D - a.rot) / 8 + (int64_t)a.Hkv * (a.D / 8);
+  const int groups = (int)((items + kRotaryThreads - 1) / kRotaryThreads);
+  // few tokens: a token's items over several blocks (N = 53: 2.6 us a launch in a graph against 3.6)
+  if ((int64_t)a.N * groups <= 8 * sm_count()) return launch_rotary_vec<DT, INTER, 1, 8>(a, groups, p_shift, s);
+  return launch_rotary_vec<DT, INTER, 4, 3>(a, groups, p_shift, s);
 }
 
 int shift_of(int p) {
@@ -469,7 +778,7 @@ int moe_add_rmsnorm(void* stream, const moe_rmsnorm_args* a) {
   if (!a->x || !a->weight || (!a->out && !a->out8) || (!a->out8 != !a->scales)) return MOE_ERR_INVALID_ARG;
   if (a->residual_out && !a->residual) return MOE_ERR_INVALID_ARG;
   if (!is_aligned(a->x, 2) || !is_aligned(a->residual, 2) || !is_aligned(a->out, 2) ||
-      !is_aligned(a->residual_out, 2) || !is_aligned(a->weight, a->weight_f32 ? 4 : 2) || !is_aligned(a->scales, 4))
+      !is_aligned(a->residual_out, 2) || !is_aligned(a->weight, a->weight_f32 ? 4 : 2) || !is_aligned(a->scales, 4) || !is_aligned(a->err, 4))
     return MOE_ERR_INVALID_ARG;
   if (a->x_stride < a->H || (a->residual && a->residual_stride < a->H) || (a->out && a->out_stride < a->H) ||
       (a->residual_out && a->residual_out_stride < a->H) || (a->out8 && a->out8_stride < a->H))
@@ -493,6 +802,7 @@ int moe_add_rmsnorm(void* stream, const moe_rmsnorm_args* a) {
   p.group = a->group;
   p.n_blocks = a->group ? (a->H + 127) / 128 : 1;
   p.eps = a->eps;
+  p.err = a->err;
   const auto ok16 = [](const void* q, int64_t stride) { return !q || (is_aligned(q, 16) && stride % 8 == 0); };
   const bool vec = a->H % 8 == 0 && ok16(a->x, a->x_stride) && ok16(a->residual, a->residual_stride) &&
                    ok16(a->out, a->out_stride) && ok16(a->residual_out, a->residual_out_stride) &&
@@ -549,8 +859,11 @@ int moe_rotary_append(void* stream, const moe_rotary_args* a) {
     return MOE_ERR_INVALID_ARG;
   OpsPdl pdl;
   const int sh = shift_of(a->page_size);
-  const cudaError_t e = a->dtype == MOE_DT_BF16 ? launch_rotary<MOE_DT_BF16>(*a, vec, sh, (cudaStream_t)stream)
-                                                : launch_rotary<MOE_DT_F16>(*a, vec, sh, (cudaStream_t)stream);
+  cudaStream_t st = (cudaStream_t)stream;
+  const cudaError_t e =
+      a->dtype == MOE_DT_BF16
+          ? (a->interleaved ? launch_rotary<MOE_DT_BF16, true>(*a, vec, sh, st) : launch_rotary<MOE_DT_BF16, false>(*a, vec, sh, st))
+          : (a->interleaved ? launch_rotary<MOE_DT_F16, true>(*a, vec, sh, st) : launch_rotary<MOE_DT_F16, false>(*a, vec, sh, st));
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

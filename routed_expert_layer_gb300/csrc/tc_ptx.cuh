@@ -88,6 +88,14 @@ __device__ __forceinline__ bool mbar_try_wait_suspended(uint64_t* bar, uint32_t 
       : "memory");
   return ok != 0;
 }
+// The same without an error word: the caller reports.
+__device__ __forceinline__ bool mbar_wait_quiet(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer() - t0 > kWaitLimitNs) return false;
+  return true;
+}
 __device__ __forceinline__ bool mbar_wait_suspended(uint64_t* bar, uint32_t parity, uint32_t* err) {
   if (mbar_try_wait_suspended(bar, parity)) return true;
   const uint64_t t0 = globaltimer();

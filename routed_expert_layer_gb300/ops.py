@@ -16,23 +16,26 @@ from . import MOE_DT_BF16, MOE_DT_F16, MOE_ERR_DEVICE_FLAG, MOE_OK, _check, lib
 
 _DT = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16}
 # the argument structs, field for field as in the header (native sizes and alignment)
-_NORM = struct.Struct("@7P5q5if").pack
+_NORM = struct.Struct("@8P5q5if").pack
 _PLAN = struct.Struct("@11Pq5i").pack
 _ROTARY = struct.Struct("@10P14q9if").pack
 _ATTN = struct.Struct("@8P11q10if").pack
-_current_stream = torch.cuda.current_stream
+# torch.cuda.current_stream and current_device build objects and check initialisation on every call: 1.3 us
+# of a call that takes 7; these are the functions under them, where this torch has them.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _I32, _F32, _F64 = torch.int32, torch.float32, torch.float64
 
 
 def _on(stream, dev: int) -> int:
-    return (_current_stream(dev) if stream is None else stream).cuda_stream
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _device(x, what: str) -> int:
     dev = x.get_device()
     if dev < 0:
         raise ValueError(f"{what}: expected a CUDA tensor")
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError(f"{what}: expected a tensor on the current device, got cuda:{dev}")
     return dev
 
@@ -65,7 +68,7 @@ def _err(err, dev: int) -> int:
 
 
 def add_rmsnorm(x, weight, eps: float, out=None, residual=None, residual_out=None, out8=None, scales=None,
-                group: int = 0, stream=None) -> None:
+                group: int = 0, err=None, stream=None) -> None:
     """t = x + residual; residual_out = t; out = y = t / sqrt(mean(t^2) + eps) * weight;
     out8 = e4m3(y / scale) with scales[row] (group 0) or scales[row][block of 128] (group 128).
 
@@ -104,7 +107,8 @@ def add_rmsnorm(x, weight, eps: float, out=None, residual=None, residual_out=Non
         sp = scales.data_ptr()
     if T <= 1:  # one row has no row stride
         xs = rs = os = ros = o8s = H
-    st = lib().moe_add_rmsnorm(_on(stream, dev), _NORM(x.data_ptr(), rp, weight.data_ptr(), op, rop, o8p, sp, xs, rs,
+    st = lib().moe_add_rmsnorm(_on(stream, dev), _NORM(x.data_ptr(), rp, weight.data_ptr(), op, rop, o8p, sp,
+                                                       0 if err is None else _err(err, dev), xs, rs,
                                                        os, ros, o8s, T, H, dt, w32, group, eps))
     if st:
         _check(st, "moe_add_rmsnorm")
