@@ -1,0 +1,79 @@
+"""The operators and the expert layer together (examples/decoder_layer.py): a layer fed whole
+prompts, chunks or single tokens over one paged cache gives the same residual stream, the
+plain 64-bit layer's, and the experts' outputs of its own norm."""
+import math
+import os
+import sys
+
+import pytest
+import torch
+
+import ops_reference as ref
+import routed_expert_layer_gb300 as rel
+import synth
+
+pytestmark = pytest.mark.gpu
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+
+LENGTHS = [150, 40, 1]
+STEPS = {"whole": [LENGTHS], "chunks": [[64, 40, 0], [80, 0, 1], [6, 0, 0]],
+         "tokens": [[120, 30, 0]] + [[1, 1, 0]] * 10 + [[20, 0, 1]]}
+
+
+def plain(layer, x, residual):
+    """The residual stream after attention of one request's tokens, in 64 bits from the same
+    bf16 inputs and weights, without intermediate roundings."""
+    f = torch.float64
+    h, n, _ = ref.norm(x, layer.norm1, 1e-6, residual)
+    qkv = n @ layer.w_qkv.to(f)
+    a, b = layer.Hq * layer.D, (layer.Hq + layer.Hkv) * layer.D
+    q, k, v = (t.view(len(x), -1, layer.D) for t in (qkv[:, :a], qkv[:, a:b], qkv[:, b:]))
+    pos = torch.arange(len(x), device="cuda")
+    q, k = (ref.rotate(t, pos, layer.inv_freq, 1.0, False)[0] for t in (q, k))
+    G = layer.Hq // layer.Hkv
+    s = torch.einsum("nhd,lhd->hnl", q, k.repeat_interleave(G, dim=1)) / math.sqrt(layer.D)
+    s = s.masked_fill(~torch.ones(len(x), len(x), dtype=torch.bool, device="cuda").tril(), -math.inf)
+    o = torch.einsum("hnl,lhd->nhd", torch.softmax(s, dim=2), v.repeat_interleave(G, dim=1))
+    return h + o.reshape(len(x), a) @ layer.w_o.to(f)
+
+
+def test_decoder_layer_in_steps():
+    from decoder_layer import DecoderLayer, run
+    H, I, E, k = 512, 256, 64, 8
+    moe = rel.MoeLayer(H, I, E, k, max_tokens=512)
+    moe.load(synth.layer(H, I, E, seed_weights=1, seed_router=2))
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    x, residual = ([torch.randn(n, H, generator=g, device="cuda").bfloat16() for n in LENGTHS] for _ in range(2))
+    for name, steps in STEPS.items():
+        layer = DecoderLayer(moe, q_heads=8, kv_heads=2, head_dim=64, requests=3, max_len=200, page_size=16)
+        out, h, m = run(layer, x, residual, LENGTHS, steps)
+        torch.cuda.synchronize()
+        assert int(layer.err.item()) == 0 and layer.attention.get_error() == 0 and moe.get_error() == 0
+        assert layer.ctx.tolist() == LENGTHS
+        used = layer.table[layer.table >= 0].tolist()
+        assert len(used) == len(set(used)) == sum(-(-n // 16) for n in LENGTHS) == int(layer.heads[0].item())
+        for r in range(3):
+            want = plain(layer, x[r], residual[r])
+            # Seven roundings to bf16 (n, qkv, rotary, weights, o, o W_o, h), each 2^-9 of its value on average at
+            # most and spread over sums of hundreds of terms; the residual stream is about 2: 2^-6 of the
+            # larger of the value and 2 holds each alone at its worst, and their sum for independent signs.
+            off = (h[r].double() - want).abs() / want.abs().clamp(min=2.0)
+            assert float(off.max()) <= 2.0 ** -6, (name, r, float(off.max()))
+            t, y, _ = ref.norm(h[r], layer.norm2, 1e-6)  # h was rounded after the norm used it
+            assert float(((m[r].double() - y).abs() / y.abs().clamp(min=1.0)).max()) <= 2.0 ** -6, (name, r)
+            again = torch.empty_like(out[r])
+            moe.forward(m[r].contiguous(), again)
+            torch.cuda.synchronize()
+            # other batch sizes take other kernels and sum orders; tokens near a routing tie may differ wholly
+            rms = float(again.float().pow(2).mean().sqrt())
+            far = ((out[r].float() - again.float()).abs().amax(dim=1) > 4e-2 * rms + 2.0 ** -7 * again.float().abs().amax(dim=1))
+            assert float(far.float().mean()) <= 0.02, (name, r)
+        layer.close()
+    moe.close()
+
+
+def test_example_runs(capsys):
+    import decoder_layer
+    decoder_layer.main()
+    assert "max difference" in capsys.readouterr().out
