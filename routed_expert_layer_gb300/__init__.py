@@ -19,6 +19,7 @@ _ROOT = os.path.dirname(_HERE)
 _CSRC = os.path.join(_HERE, "csrc")
 _BUILD = os.path.join(_HERE, "_build")
 LIB_PATH = os.path.join(_BUILD, "libmoe_gb300.so")
+BINDING_PATH = os.path.join(_BUILD, "_ops_binding.so")  # CPython binding of the operators in ops.py
 _SOURCES = ["api.cu", "route.cu", "router_tc.cu", "expert_tc.cu", "noalloc.cu", "block.cu", "ops.cu", "attn.cu"]
 _HEADERS = ["moe_internal.cuh", "tc_ptx.cuh", "ops_internal.cuh"]
 _INCLUDES = ["moe_gb300.h", "moe_ops_gb300.h"]
@@ -59,6 +60,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     deps += [os.path.join(_ROOT, "include", f) for f in _INCLUDES]
     newest = max(os.path.getmtime(d) for d in deps)
     if not force and os.path.exists(LIB_PATH) and os.path.getmtime(LIB_PATH) >= newest:
+        _build_binding(force, newest)
         return LIB_PATH
     nvcc = _nvcc()
 
@@ -79,7 +81,29 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    _build_binding(True, newest)
     return LIB_PATH
+
+
+def _build_binding(force: bool, newest: float) -> None:
+    """Compile csrc/binding.cpp against the installed PyTorch's headers (host code only, seconds)."""
+    import importlib.util
+    import sysconfig
+    src = os.path.join(_CSRC, "binding.cpp")
+    if not force and os.path.exists(BINDING_PATH) and os.path.getmtime(BINDING_PATH) >= max(newest, os.path.getmtime(src)):
+        return
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda"
+    inc = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    tmp = BINDING_PATH + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", *[f"-I{d}" for d in inc], src, "-o", tmp,
+           f"-L{_BUILD}", "-l:libmoe_gb300.so", f"-L{os.path.join(torch_dir, 'lib')}", "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stderr}")
+    os.replace(tmp, BINDING_PATH)
 
 
 class Config(ctypes.Structure):
@@ -132,12 +156,11 @@ def lib():
         L.moe_launch_count.restype = ctypes.c_int64
         L.moe_launch_count.argtypes = [vp]
         L.moe_route_noalloc.argtypes = [vp, p, p, p, i32, i32, i32, i32, p, p, p, p, p, p, p]
-        packed = ctypes.c_char_p  # argument structs packed by ops.py
-        L.moe_add_rmsnorm.argtypes = [vp, packed]
-        L.moe_paged_plan.argtypes = [vp, packed]
-        L.moe_rotary_append.argtypes = [vp, packed]
+        L.moe_add_rmsnorm.argtypes = [vp, p]
+        L.moe_paged_plan.argtypes = [vp, p]
+        L.moe_rotary_append.argtypes = [vp, p]
         L.moe_attn_create.argtypes = [ctypes.c_int, ctypes.POINTER(vp)]
-        L.moe_attn_forward.argtypes = [vp, vp, packed]
+        L.moe_attn_forward.argtypes = [vp, vp, p]
         L.moe_attn_get_error.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
         L.moe_attn_device_bytes.restype = ctypes.c_int64
         L.moe_attn_device_bytes.argtypes = [vp]

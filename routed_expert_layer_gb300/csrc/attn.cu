@@ -967,7 +967,8 @@ int attn_check(const moe_attn_args* a) {
                              a->Hkv};
   for (int i = 0; i < 10; ++i) {
     const int64_t s = strides[i];
-    if (s < 0 || s % 8 || s >= ((int64_t)1 << 38) || (s == 0 && extents[i] > 1)) return MOE_ERR_INVALID_ARG;
+    // (the stride of a dimension of one is never used)
+    if (s < 0 || s >= ((int64_t)1 << 38) || (extents[i] > 1 && (s == 0 || s % 8))) return MOE_ERR_INVALID_ARG;
   }
   const void* t32[] = {a->block_table, a->q_start, a->kv_lens};
   for (const void* p : t32)
