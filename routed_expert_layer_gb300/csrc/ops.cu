@@ -752,7 +752,8 @@ cudaError_t launch_rotary(const moe_rotary_args& a, bool vec, int p_shift, cudaS
   const int64_t items = (int64_t)(a.Hq + a.Hkv) * ((INTER ? a.rot : a.rot / 2) + a.D - a.rot) / 8 + (int64_t)a.Hkv * (a.D / 8);
   const int groups = (int)((items + kRotaryThreads - 1) / kRotaryThreads);
   // few tokens: a token's items over several blocks (N = 53: 2.6 us a launch in a graph against 3.6)
-  if ((int64_t)a.N * groups <= 8 * sm_count()) return launch_rotary_vec<DT, INTER, 1, 8>(a, groups, p_shift, s);
+  if (groups == 1 || (int64_t)a.N * groups <= 8 * sm_count()) return launch_rotary_vec<DT, INTER, 1, 8>(a, groups, p_shift, s);
+  if (groups == 2) return launch_rotary_vec<DT, INTER, 2, 6>(a, groups, p_shift, s);
   return launch_rotary_vec<DT, INTER, 4, 3>(a, groups, p_shift, s);
 }
 
