@@ -129,9 +129,10 @@ MOE_API int moe_rotary_append(void* stream, const moe_rotary_args* a);
  * A row that sees no key (kv_lens < new) gets zeros and lse = -inf. Keys a row does not
  * see never reach it, whatever they hold. fp32 scores and sums; the weights are rounded to
  * dtype for the second product. Rows of q outside every request are not written.
- * A page outside [0, num_pages) or past the table raises MOE_OPS_ERR_INDEX and counts as
- * zeros; a request whose rows lie outside [0, N] raises it and is skipped.
- * D is 64 or 128, Hq % Hkv == 0, Hq / Hkv <= 128, P a power of two of 16 to 1024,
+ * A page outside [0, num_pages) raises MOE_OPS_ERR_INDEX and counts as zeros; kv_lens beyond the
+ * table's W * P raises it and counts as W * P (below 0: as 0); a request whose rows lie outside
+ * [0, N] raises it and is skipped.
+ * D is 64 or 128, Hq % Hkv == 0, Hq / Hkv <= 128, P a power of two of 16 to 1024, W * P < 2^30,
  * pointers 16-byte aligned and strides multiples of 8 elements (lse, tables: 4 bytes),
  * scale > 0, out must not overlap q. max_new: the most new tokens a request of this call
  * has, if known, else 0; it chooses a variant and never changes what is computed. */

@@ -28,11 +28,22 @@
 // P is rounded to the type of the cache for the second product (the tensor cores take no
 // other); l sums the unrounded values.
 //
-// Two instances per head width. Where every request has at most 128 rows (decoding, a few
-// draft tokens) the call streams the cache: one tile, 64 keys per step, two CTAs per SM, so one
-// CTA's softmax and its items' ends hide behind the other's loads. Longer chunks are bound
-// by the tensor cores and the exponentials: two tiles per CTA, 128 keys per step; the MMAs
-// of one tile run under the softmax of the other, and every K and V tile is used twice.
+// Two instances per head width, chosen by the most rows a request can have (max_new, or all of N):
+// up to one tile's tokens, or more.
+//   One row tile, 64 keys per step, two CTAs per SM: decoding and a few draft tokens stream the cache, so one
+//   CTA's softmax and items' ends hide behind the other's loads. 128 requests of 500 to 7,500 keys, 96 heads
+//   over 8 of 128, bf16: 318 to 326 us, 6.4 to 6.6 TB/s, bound by memory.
+//   Two row tiles, 128 keys per step, one CTA per SM: every K and V tile is used twice, and one tile's
+//   products run under the other's softmax. A chunk of 4,096 tokens over 16,384 keys, the same heads:
+//   1.89 ms, 1.53 PFLOP/s. Bound by the chain of a row tile's step: softmax 1,550 cycles (512 of them the
+//   exponentials' at 4 per instruction), handing over 200, and the MMAs after the last weights 1,040, of
+//   which each row tile's half overlaps the other's.
+// Measured on the way, same chunk: a thread chosen by lane number instead of elect.sync issues an MMA every 85
+// cycles instead of 45 (2.47 ms); a row split over two warps 2.28 ms (the exchange costs what the shorter
+// rows gain); one issuing thread per row tile 2.08 ms; waiting for the next tiles between the two row
+// tiles' MMAs 2.27 ms (a wait behind queued MMAs lets the pipe run dry); the exponential in 16 bits is no
+// faster; a second S tile per row tile with one row tile per CTA 440 us against 326 for decoding; output rows
+// staged through shared memory 1.99 ms.
 #include <algorithm>
 #include <numeric>
 
@@ -44,6 +55,7 @@ struct moe_attn_ctx {
   int sm_count = 0;
   void* mem = nullptr;
   size_t bytes = 0;
+  size_t head_bytes = 0;  // error word and tickets
   uint32_t* err = nullptr;
   int32_t* tickets = nullptr;
   float* parts = nullptr;
@@ -59,9 +71,10 @@ constexpr int kRows = 128;          // rows of a tile (TMEM lanes)
 constexpr int kRuns = 128;          // runs of requests whose cost sums a CTA keeps
 constexpr int kMinStretch = 256;    // a CTA's least share of the axis (in keys): more CTAs than that are not worth a join
 constexpr int kWhole = 768;         // where a CTA's share is less than twice this, items up to this long are not split
-// What an item's start and end cost, in keys. With one row tile they hide behind the other CTA of the SM.
+// What the start and end of an item of so many rows cost, in keys. With one row tile they hide behind the
+// other CTA of the SM; with two, O's way out and the join of a full tile cost as much as some keys.
 template <int QT>
-constexpr int kItemCost = QT == 1 ? 128 : 384;
+__device__ __forceinline__ int item_cost(int rows) { return QT == 1 ? 128 : 256 + rows; }
 constexpr int kNoteSlots = 8;       // pieces whose notes of non-finite tokens are kept (> V stages + 2)
 constexpr float kRescaleLog2 = 8.f;
 
@@ -119,13 +132,15 @@ struct Work {
   int b, h, i;             // request, key head, tile group
   int n_new, ctx, q0;      // new tokens, cached tokens before them (negative: rows without keys), first row of q
   int n_items;             // tile groups
+  int fixed;               // an item's start and end, in keys
   int64_t head_cost;       // cost of one key head of the request
   int64_t base, at, cost;  // axis: start of the head, start and length of the item
 
   template <int QT>
-  __device__ __forceinline__ bool load(const AttnParams& p, int request) {  // false: rows outside q
+  __device__ __forceinline__ bool load(const AttnParams& p, int request) {  // false: rows outside q, or keys past the table
     b = request;
-    const int s = p.a.q_start[b], e = p.a.q_start[b + 1], kv = max(p.a.kv_lens[b], 0);
+    const int s = p.a.q_start[b], e = p.a.q_start[b + 1], most = p.a.W << p.p_shift, len = p.a.kv_lens[b];
+    const int kv = min(max(len, 0), most);
     const bool ok = s >= 0 && e <= p.a.N && e >= s;
     n_new = ok ? e - s : 0;
     q0 = s;
@@ -133,13 +148,14 @@ struct Work {
     const int st = QT * p.tpt;
     n_items = (n_new + st - 1) / st;
     const int64_t n = n_items;
-    head_cost = n * (kItemCost<QT> + max(ctx, 0)) + st * (n * (n - 1) / 2) + n_new;
-    return ok;
+    fixed = item_cost<QT>(min(n_new, st) * p.G);
+    head_cost = n * (fixed + max(ctx, 0)) + st * (n * (n - 1) / 2) + n_new;
+    return ok && len <= most;
   }
   template <int QT>
   __device__ __forceinline__ void set_item(const AttnParams& p, int64_t before) {
     at = base + before;
-    cost = kItemCost<QT> + max(ctx, 0) + min((i + 1) * QT * p.tpt, n_new);
+    cost = fixed + max(ctx, 0) + min((i + 1) * QT * p.tpt, n_new);
   }
   // The item at x, by a whole warp (every lane gets it).
   template <int QT>
@@ -157,7 +173,7 @@ struct Work {
     }
     h = (int)div_floor(x - acc, head_cost);
     base = acc + h * head_cost;
-    const int64_t rest = x - base, each = kItemCost<QT> + max(ctx, 0), st = QT * p.tpt;
+    const int64_t rest = x - base, each = fixed + max(ctx, 0), st = QT * p.tpt;
     int hi = n_items;
     lo = 0;
     while (hi - lo > 1) {  // the last group that starts at or before rest
@@ -203,14 +219,14 @@ struct Piece {
     kv_end = max(0, w.ctx + min(tok + QT * p.tpt, w.n_new));
     first_lim = w.ctx + tok + 1;
     const int nt = (kv_end + BN - 1) / BN;
-    first_part = w.cost <= max(ax.whole, (int64_t)kItemCost<QT> + BN) ? w.cost : kItemCost<QT> + BN;
+    first_part = w.cost <= max(ax.whole, (int64_t)w.fixed + BN) ? w.cost : w.fixed + BN;
     int64_t lo = max(ax.x0 - w.at, (int64_t)0), hi = min(ax.x1 - w.at, w.cost);
     if (lo < first_part) lo = 0;
     if (hi < first_part) hi = 0;
     none = hi == 0;
     split = lo > 0 || hi < w.cost;
-    t0 = (int)min((int64_t)nt, max(lo - kItemCost<QT>, (int64_t)0) / BN);
-    t1 = none ? t0 : hi == w.cost ? nt : (int)min((int64_t)nt, max(hi - kItemCost<QT>, (int64_t)0) / BN);
+    t0 = (int)min((int64_t)nt, max(lo - w.fixed, (int64_t)0) / BN);
+    t1 = none ? t0 : hi == w.cost ? nt : (int)min((int64_t)nt, max(hi - w.fixed, (int64_t)0) / BN);
 #pragma unroll
     for (int q = 0; q < QT; ++q) {
       const int end = tok + q * p.tpt < w.n_new ? max(0, w.ctx + min(tok + (q + 1) * p.tpt, w.n_new)) : 0;
@@ -419,8 +435,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
           const int64_t key = (int64_t)t * BN + (int64_t)lane * P;
           int id = p.a.num_pages;
           if (lane < pages && key < pc.kv_end) {
-            const int64_t col = key >> p.p_shift;
-            id = col < p.a.W ? table[col] : -1;
+            id = table[key >> p.p_shift];  // kv_end is within the table
             if (id < 0 || id >= p.a.num_pages) {
               atomicOr(p.err, kErrIndex);
               id = p.a.num_pages;
@@ -462,7 +477,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
       for (uint32_t j = vn > NV ? vn - NV : 0; j < vn; ++j) warp_wait(&vfull[j % NV], (j / NV) & 1, p.err);
     }
   } else if (warp == 1) {
-    // ---- MMA issuer ----
+    // ---- MMA issuer. The MMAs of one thread run in the order of issue: P(t) is read before S(t + 1) is
+    // written over it, and what a commit reports includes every MMA before it. ----
     if (elect_one()) {
       constexpr uint32_t kIdS = idesc_16(DT == MOE_DT_BF16, false, kRows, BN);
       constexpr uint32_t kIdO = idesc_16(DT == MOE_DT_BF16, true, kRows, D);
@@ -955,7 +971,7 @@ int attn_check(const moe_attn_args* a) {
   if (a->dtype != MOE_DT_BF16 && a->dtype != MOE_DT_F16) return MOE_ERR_INVALID_ARG;
   if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return MOE_ERR_INVALID_ARG;
   if ((a->D != 64 && a->D != 128) || a->Hq / a->Hkv > 128 || a->page_size < 16 || a->page_size > 1024 ||
-      (int64_t)a->W * a->page_size >= ((int64_t)1 << 31) || (int64_t)a->N * a->Hq >= ((int64_t)1 << 31))
+      (int64_t)a->W * a->page_size >= ((int64_t)1 << 30) || (int64_t)a->N * a->Hq >= ((int64_t)1 << 31))
     return MOE_ERR_UNSUPPORTED;
   if (a->N == 0) return MOE_OK;
   const void* t16[] = {a->q, a->k_cache, a->v_cache, a->out};
@@ -1004,6 +1020,7 @@ int moe_attn_create(int device, moe_attn_ctx** out) {
   // error word | tickets (one per CTA and row tile) | partial results (two per CTA and row tile)
   const size_t most = 2 * (size_t)c->sm_count;
   const size_t head = (256 + most * 4 + 255) / 256 * 256;
+  c->head_bytes = head;
   c->bytes = head + 2 * most * sizeof(float) * StreamCfg<0, 128>::kPart;
   if (cudaMalloc(&c->mem, c->bytes) != cudaSuccess) {
     cudaGetLastError();
@@ -1058,7 +1075,8 @@ int moe_attn_get_error(moe_attn_ctx* ctx, uint32_t* bits) {
   uint32_t v = 0;
   if (cudaDeviceSynchronize() != cudaSuccess) return MOE_ERR_CUDA;
   if (cudaMemcpy(&v, ctx->err, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
-  if (cudaMemset(ctx->err, 0, sizeof(v)) != cudaSuccess) return MOE_ERR_CUDA;
+  // a kernel that gave up leaves its tickets behind
+  if (v && cudaMemset(ctx->mem, 0, ctx->head_bytes) != cudaSuccess) return MOE_ERR_CUDA;
   if (bits) *bits = v;
   return v ? MOE_ERR_DEVICE_FLAG : MOE_OK;
 }
