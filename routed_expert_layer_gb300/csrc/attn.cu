@@ -69,8 +69,8 @@ namespace {
 
 constexpr int kRows = 128;          // rows of a tile (TMEM lanes)
 constexpr int kRuns = 128;          // runs of requests whose cost sums a CTA keeps
-constexpr int kMinStretch = 256;    // a CTA's least share of the axis (in keys): more CTAs than that are not worth a join
-constexpr int kWhole = 768;         // where a CTA's share is less than twice this, items up to this long are not split
+constexpr int kMinStretch = 192;    // a CTA's least share of the axis (in keys): more CTAs than that are not worth a join
+constexpr int kWhole = 512;         // where a CTA's share is less than twice this, items up to this long are not split
 // What the start and end of an item of so many rows cost, in keys. With one row tile they hide behind the
 // other CTA of the SM; with two, O's way out and the join of a full tile cost as much as some keys.
 template <int QT>
@@ -431,21 +431,26 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         }
         __syncwarp();
         const int32_t* table = p.a.block_table + w.b * p.a.table_stride;
-        auto page_of = [&](int t) {  // this lane's page of tile t
-          const int64_t key = (int64_t)t * BN + (int64_t)lane * P;
-          int id = p.a.num_pages;
-          if (lane < pages && key < pc.kv_end) {
-            id = table[key >> p.p_shift];  // kv_end is within the table
-            if (id < 0 || id >= p.a.num_pages) {
-              atomicOr(p.err, kErrIndex);
-              id = p.a.num_pages;
-            }
-          }
-          return id;
+        // pages are looked up 32 at a time, the next 32 while these are copied
+        const auto inside = [&](int col) { return ((int64_t)col << p.p_shift) < pc.kv_end; };  // (the table holds kv_end)
+        const auto look_up = [&](int col) { return inside(col + lane) ? table[col + lane] : 0; };
+        const auto checked = [&](int col, int page) {  // num_pages: nothing there, TMA fills with zeros
+          if (!inside(col + lane)) return p.a.num_pages;
+          if (page >= 0 && page < p.a.num_pages) return page;
+          atomicOr(p.err, kErrIndex);
+          return p.a.num_pages;
         };
-        int id = page_of(pc.t0);
+        int col0 = (int)(((int64_t)pc.t0 * BN) >> p.p_shift);
+        int ids = checked(col0, look_up(col0)), ids_next = look_up(col0 + 32);
         for (int t = pc.t0; t < pc.t1 && ok; ++t) {
-          const int id_next = t + 1 < pc.t1 ? page_of(t + 1) : 0;
+          int at = (int)(((int64_t)t * BN) >> p.p_shift) - col0;
+          if (at >= 32) {
+            col0 += 32;
+            at -= 32;
+            ids = checked(col0, ids_next);
+            ids_next = look_up(col0 + 32);
+          }
+          const int id = __shfl_sync(0xFFFFFFFFu, ids, (at + lane) & 31);  // lanes below `pages`: the tile's pages
           const int row = P >= BN ? (t * BN) & (P - 1) : 0;
           const int ks = (int)(kn % NK), vs = (int)(vn % NV);
           ok = warp_wait(&kempty[ks], ((kn / NK) & 1) ^ 1u, p.err);
@@ -466,7 +471,6 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
             for (int d = 0; d < D / 64; ++d)
               tma_4d(sv + vs * C::kTile + d * C::kBlk + lane * rows * 128, &map_v, d * 64, row, w.h, id, &vfull[vs]);
           ++vn;
-          id = id_next;
         }
       }
       advance();
@@ -827,11 +831,61 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         if (join) {
           __threadfence();
           if (r == 0) p.tickets[first * QT + q] = 0;
-          // Lane = row, each warp a quarter of the columns, pieces in key order, two at a time (their
-          // loads overlap).
-          constexpr int kCols4 = D / 16;
           const int rows = n_tok * p.G;
+          const auto piece_at = [&](int k) {
+            return p.parts + (size_t)((2 * (first + k) + (k == 0 ? 1 : 0)) * QT + q) * C::kPart;
+          };
+          const auto row_out = [&](int row, int64_t& n, int& hd) {  // token and head of a row of the tile
+            const int t = row / p.G;
+            n = (int64_t)w.q0 + tok + t;
+            hd = w.h * p.G + row - t * p.G;
+          };
+          const auto row_lse = [&](float top, float sum) {
+            return sum == 0.f ? -INFINITY : (top * p.scale_log2 + log2f(sum)) * 0.69314718055994530942f;
+          };
+          if (rows <= 32) {
+            // Few rows, perhaps many pieces (one long request): four columns of a row per thread, neighbours on
+            // neighbouring rows, eight pieces' loads at once.
+            constexpr int kAtOnce = 8;
+            for (int x = r; x < rows * (D / 4); x += kRows) {
+              const int c = x / rows, row = x - c * rows;
+              float top = -INFINITY, sum = 0.f;
+              float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+              for (int k = 0; k < pieces; k += kAtOnce) {
+                float mk[kAtOnce], lk[kAtOnce];
+                float4 o[kAtOnce];
+#pragma unroll
+                for (int u = 0; u < kAtOnce; ++u) {
+                  const float* pt = piece_at(min(k + u, pieces - 1));
+                  mk[u] = __ldcg(pt + kRows * D + row);
+                  lk[u] = k + u < pieces ? __ldcg(pt + kRows * (D + 1) + row) : 0.f;
+                  o[u] = __ldcg(reinterpret_cast<const float4*>(pt) + c * kRows + row);
+                }
+#pragma unroll
+                for (int u = 0; u < kAtOnce; ++u) {
+                  if (lk[u] == 0.f) continue;  // the row saw nothing in this piece; its O may not be written
+                  const float nt = fmaxf(top, mk[u]);
+                  const float f0 = ex2((top - nt) * p.scale_log2), f = ex2((mk[u] - nt) * p.scale_log2);
+                  top = nt;
+                  sum = sum * f0 + lk[u] * f;
+                  acc.x = acc.x * f0 + o[u].x * f;
+                  acc.y = acc.y * f0 + o[u].y * f;
+                  acc.z = acc.z * f0 + o[u].z * f;
+                  acc.w = acc.w * f0 + o[u].w * f;
+                }
+              }
+              const float inv = sum == 0.f ? 0.f : 1.f / sum;
+              int64_t n;
+              int hd;
+              row_out(row, n, hd);
+              *reinterpret_cast<uint2*>((uint16_t*)p.a.out + n * p.a.out_tok + (int64_t)hd * p.a.out_head + 4 * c) =
+                  make_uint2(pack2<DT>(acc.x * inv, acc.y * inv), pack2<DT>(acc.z * inv, acc.w * inv));
+              if (p.a.lse && c == 0) p.a.lse[n * p.a.Hq + hd] = row_lse(top, sum);
+            }
+          } else
+          // Lane = row, each warp a quarter of the columns, two pieces at a time.
           for (int r0 = 0; r0 < rows; r0 += 32) {
+            constexpr int kCols4 = D / 16;
             const int row = min(r0 + lane, rows - 1);
             float top = -INFINITY, sum = 0.f;
             float4 acc[kCols4];
@@ -842,8 +896,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
               float4 o[2][kCols4];
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
-                const int kk = min(k + u, pieces - 1);
-                const float* pt = p.parts + (size_t)((2 * (first + kk) + (kk == 0 ? 1 : 0)) * QT + q) * C::kPart;
+                const float* pt = piece_at(min(k + u, pieces - 1));
                 mk[u] = __ldcg(pt + kRows * D + row);
                 lk[u] = k + u < pieces ? __ldcg(pt + kRows * (D + 1) + row) : 0.f;
 #pragma unroll
@@ -868,8 +921,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
             }
             if (r0 + lane >= rows) continue;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            const int t = row / p.G, hd = w.h * p.G + row - t * p.G;
-            const int64_t n = (int64_t)w.q0 + tok + t;
+            int64_t n;
+            int hd;
+            row_out(row, n, hd);
             uint16_t* out = (uint16_t*)p.a.out + n * p.a.out_tok + (int64_t)hd * p.a.out_head + quarter * (D / 4);
 #pragma unroll
             for (int j = 0; j < kCols4; j += 2)
@@ -877,9 +931,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
                   make_uint4(pack2<DT>(acc[j].x * inv, acc[j].y * inv), pack2<DT>(acc[j].z * inv, acc[j].w * inv),
                              pack2<DT>(acc[j + 1].x * inv, acc[j + 1].y * inv),
                              pack2<DT>(acc[j + 1].z * inv, acc[j + 1].w * inv));
-            if (p.a.lse && quarter == 0)
-              p.a.lse[n * p.a.Hq + hd] =
-                  sum == 0.f ? -INFINITY : (top * p.scale_log2 + log2f(sum)) * 0.69314718055994530942f;
+            if (p.a.lse && quarter == 0) p.a.lse[n * p.a.Hq + hd] = row_lse(top, sum);
           }
         }
       }
