@@ -2,6 +2,7 @@
 // step's plan, rotary positions with the cache append. Interfaces and formulas:
 // include/moe_ops_gb300.h.
 #include <algorithm>
+#include <type_traits>
 
 #include "ops_internal.cuh"
 #include "tc_ptx.cuh"
@@ -26,33 +27,37 @@ struct NormParams {
   uint32_t* err;
 };
 
-template <int DT, int VEC>
-__device__ __forceinline__ void load_vec(const uint16_t* p, float (&v)[VEC]) {
-  if constexpr (VEC == 8) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// A piece of 8, 4, 2 or 1 elements as it lies in memory.
+template <int N>
+using Piece = std::conditional_t<N == 8, uint4, std::conditional_t<N == 4, uint2, std::conditional_t<N == 2, uint32_t, uint16_t>>>;
+
+template <int DT, int N>
+__device__ __forceinline__ void unpack(const Piece<N>& w, float (&v)[N]) {
+  if constexpr (N == 1) {
+    v[0] = to_f32<DT>(w);
+  } else {
+    uint32_t u[N / 2];
+    if constexpr (N == 2) u[0] = w;
+    else u[0] = w.x, u[1] = w.y;
+    if constexpr (N == 8) u[2] = w.z, u[3] = w.w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N / 2; ++i) {
       const float2 f = unpack2<DT>(u[i]);
       v[2 * i] = f.x;
       v[2 * i + 1] = f.y;
     }
-  } else {
-    v[0] = to_f32<DT>(*p);
   }
 }
 
-template <int DT, int VEC>
-__device__ __forceinline__ void store_vec(uint16_t* p, const float (&v)[VEC]) {
-  if constexpr (VEC == 8) {
-    uint4 w;
-    w.x = pack2<DT>(v[0], v[1]);
-    w.y = pack2<DT>(v[2], v[3]);
-    w.z = pack2<DT>(v[4], v[5]);
-    w.w = pack2<DT>(v[6], v[7]);
-    *reinterpret_cast<uint4*>(p) = w;
-  } else {
+template <int DT, int N>
+__device__ __forceinline__ void store_vec(uint16_t* p, const float (&v)[N]) {
+  if constexpr (N == 1) {
     *p = from_f32<DT>(v[0]);
+  } else {
+    Piece<N> w;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) reinterpret_cast<uint32_t*>(&w)[i] = pack2<DT>(v[2 * i], v[2 * i + 1]);
+    *reinterpret_cast<Piece<N>*>(p) = w;
   }
 }
 
@@ -102,21 +107,14 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
 // registers 95 us; two blocks per SM with 2, 3, 4 stages 86.1, 87.1, 87.5 us, one block with six 111 us,
 // three blocks of 224 threads 97 us. Single rows too: T = 1 2.4 us a launch in a graph (register loads 2.9).
 // norm_rows_kernel (H <= 1024, 16-byte chunks): several rows per block, one chunk per thread, the next
-// rows' loads issued before this one's reduction; staging rows this short would cost a copy each.
-// norm_any_kernel: one element per chunk, for any width, stride and alignment.
+// rows' loads issued before this one's reduction; staging rows this short would cost a copy each. Both at
+// T = 8192: H = 128 4.5 us (staged 6.3), 512 7.6 (8.4), 1024 13.1 (13.1); T = 1, H = 512 1.8 us (2.6).
+// norm_any_kernel (chunks of 2 or 1 elements): what is wider than 14336, or whose width, stride or alignment is
+// not a multiple of 8. T = 8192: H = 7170 bf16 with residual 78 us, 7169 with 8-bit blocks 209 us, bound by
+// the number of its 1- and 2-byte accesses. Where all three can run, in elements, pairs and by the kernels above:
+// H = 7168 196, 102, 88 us, H = 1024 22.4, 22.7, 13.2, T = 1 of 7168 5.4, 4.3, 3.3.
 
 __device__ __forceinline__ uint4 load16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
-
-template <int DT>
-__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack2<DT>(u[i]);
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
-}
 
 // The 8-bit output and scales of a row whose chunks are in t (|t| up to mx in this thread), by the whole block.
 template <int NV>
@@ -185,10 +183,10 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_rows_kernel(const NormParams 
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = (tx + i * TX) * 8;
-      unpack8<DT>(x[i], t[i]);
+      unpack<DT, 8>(x[i], t[i]);
       if (p.residual) {
         float a[8];
-        unpack8<DT>(r[i], a);
+        unpack<DT, 8>(r[i], a);
 #pragma unroll
         for (int j = 0; j < 8; ++j) t[i][j] += a[j];
         if (p.residual_out && live && e < H) store_vec<DT, 8>(p.residual_out + row * p.residual_out_stride + e, t[i]);
@@ -209,7 +207,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_rows_kernel(const NormParams 
 #pragma unroll
         for (int j = 0; j < 8; ++j) g[j] = e < H ? __ldg(reinterpret_cast<const float*>(p.weight) + e + j) : 0.f;
       } else {
-        unpack8<DT>(w[i], g);
+        unpack<DT, 8>(w[i], g);
       }
       const bool in = live && e < H;
 #pragma unroll
@@ -271,10 +269,10 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_staged_kernel(const NormParam
     for (int i = 0; i < NV; ++i) {
       const int c = tx + i * TX;
       const bool in = c * 8 < H;
-      unpack8<DT>(in ? *reinterpret_cast<const uint4*>(d + c * 16) : make_uint4(0, 0, 0, 0), t[i]);
+      unpack<DT, 8>(in ? *reinterpret_cast<const uint4*>(d + c * 16) : make_uint4(0, 0, 0, 0), t[i]);
       if (p.residual && in) {
         float a[8];
-        unpack8<DT>(*reinterpret_cast<const uint4*>(d + row_bytes + c * 16), a);
+        unpack<DT, 8>(*reinterpret_cast<const uint4*>(d + row_bytes + c * 16), a);
 #pragma unroll
         for (int j = 0; j < 8; ++j) t[i][j] += a[j];
       }
@@ -301,7 +299,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_staged_kernel(const NormParam
 #pragma unroll
         for (int j = 0; j < 8; ++j) g[j] = __ldg(reinterpret_cast<const float*>(p.weight) + e + j);
       } else {
-        unpack8<DT>(w[i], g);
+        unpack<DT, 8>(w[i], g);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -319,66 +317,124 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_staged_kernel(const NormParam
   }
 }
 
-template <int DT, int NV>
-__global__ void __launch_bounds__(1024) norm_any_kernel(const NormParams p) {
-  __shared__ float red_sum[32];
-  __shared__ uint32_t red_max[32];
-  extern __shared__ uint32_t block_max[];  // with blocks of 128: [block rows][n_blocks]
+// The pieces of a row are VE elements, thread tx has pieces tx, tx + TX, ... (NV of them). TX is a constant, so a
+// thread keeps one address per tensor, and no store stands between loads, which would wait for it.
+template <int DT, int VE, int TX, int NV, int MINB>
+__global__ void __launch_bounds__(TX < 256 ? 256 : TX, MINB) norm_any_kernel(const NormParams p) {
+  __shared__ float red_sum[2][32];
+  __shared__ uint32_t red_max[2][32];
+  extern __shared__ uint32_t block_max[];  // with blocks of 128: [block rows][n_blocks] maxima, then 1 / scale
   pdl_entry();
-  const int tx = threadIdx.x, TX = blockDim.x, H = p.H;
-  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  const bool live = row < p.T;
-  float t[NV];
-  float ss = 0.f;
+  const int tx = threadIdx.x, n_pieces = p.H / VE;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  const auto place = [&](int i) { return (tx + i * TX) * VE; };
+  int turn = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < p.T; r0 += step, turn ^= 1) {
+    const bool live = r0 + threadIdx.y < p.T;
+    const int64_t row = live ? r0 + threadIdx.y : p.T - 1;
+    const int n = live ? n_pieces : 0;
+    float t[NV][VE];
+    {
+      Piece<VE> a[NV];
+      const uint16_t* x = p.x + row * p.x_stride;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = tx + i * TX;
-    t[i] = 0.f;
-    if (live && e < H) {
-      t[i] = to_f32<DT>(p.x[row * p.x_stride + e]);
+      for (int i = 0; i < NV; ++i) a[i] = tx + i * TX < n ? *reinterpret_cast<const Piece<VE>*>(x + place(i)) : 0;
       if (p.residual) {
-        t[i] += to_f32<DT>(p.residual[row * p.residual_stride + e]);
-        if (p.residual_out) p.residual_out[row * p.residual_out_stride + e] = from_f32<DT>(t[i]);
-      }
-      ss = fmaf(t[i], t[i], ss);
-    }
-  }
-  const float rs = rsqrtf(row_sum(ss, red_sum) / (float)H + p.eps);
-  uint32_t mx = 0;
+        Piece<VE> b[NV];
+        const uint16_t* r = p.residual + row * p.residual_stride;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = tx + i * TX;
-    if (live && e < H) {
-      const float w = p.weight_f32 ? reinterpret_cast<const float*>(p.weight)[e]
-                                   : to_f32<DT>(reinterpret_cast<const uint16_t*>(p.weight)[e]);
-      t[i] = t[i] * rs * w;
-      mx = max(mx, abs_bits(t[i]));
-      if (p.out) p.out[row * p.out_stride + e] = from_f32<DT>(t[i]);
+        for (int i = 0; i < NV; ++i) b[i] = tx + i * TX < n ? *reinterpret_cast<const Piece<VE>*>(r + place(i)) : 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          float c[VE];
+          unpack<DT, VE>(a[i], t[i]);
+          unpack<DT, VE>(b[i], c);
+#pragma unroll
+          for (int j = 0; j < VE; ++j) t[i][j] += c[j];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) unpack<DT, VE>(a[i], t[i]);
+      }
     }
-  }
-  if (!p.out8) return;
-  uint32_t* bm = block_max + threadIdx.y * p.n_blocks;
-  if (p.group == 0) {
-    mx = row_max(mx, red_max);
-    if (live && tx == 0) p.scales[row] = __uint_as_float(mx) / 448.f;
-  } else {
-    for (int b = tx; b < p.n_blocks; b += TX) bm[b] = 0;
-    __syncthreads();
+    if (p.residual_out) {
+      uint16_t* o = p.residual_out + row * p.residual_out_stride;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (tx + i * TX < n) store_vec<DT, VE>(o + place(i), t[i]);
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < VE; ++j)
+        ss = fmaf(t[i][j], t[i][j], ss);
+    const float rs = rsqrtf(row_sum(ss, red_sum[turn]) / (float)p.H + p.eps);
+    if (p.weight_f32) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < VE; ++j)
+          t[i][j] = t[i][j] * rs * (tx + i * TX < n ? __ldg(reinterpret_cast<const float*>(p.weight) + place(i) + j) : 0.f);
+    } else {
+      Piece<VE> a[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        a[i] = tx + i * TX < n ? *reinterpret_cast<const Piece<VE>*>(reinterpret_cast<const uint16_t*>(p.weight) + place(i)) : 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float c[VE];
+        unpack<DT, VE>(a[i], c);
+#pragma unroll
+        for (int j = 0; j < VE; ++j) t[i][j] = t[i][j] * rs * c[j];
+      }
+    }
+    if (p.out) {
+      uint16_t* o = p.out + row * p.out_stride;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (tx + i * TX < n) store_vec<DT, VE>(o + place(i), t[i]);
+    }
+    if (!p.out8) continue;
+    uint32_t* bm = block_max + threadIdx.y * p.n_blocks;
+    float inv = 1.f;
+    if (p.group == 0) {
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < VE; ++j) mx = max(mx, tx + i * TX < n ? abs_bits(t[i][j]) : 0);
+      const float s = __uint_as_float(row_max(mx, red_max[turn])) / 448.f;
+      if (live && tx == 0) p.scales[row] = s;
+      inv = s > 0.f ? 1.f / s : 1.f;  // zeros stay zeros; a NaN scale keeps its NaN values
+    } else {
+      for (int b = tx; b < p.n_blocks; b += TX) bm[b] = 0;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {  // a warp's 32 pieces lie in one block of 128
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < VE; ++j) m = max(m, tx + i * TX < n ? abs_bits(t[i][j]) : 0);
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+        if ((tx & 31) == 0 && tx + i * TX < n) atomicMax(&bm[place(i) >> 7], m);
+      }
+      __syncthreads();
+      for (int b = tx; b < p.n_blocks; b += TX) {
+        const float s = __uint_as_float(bm[b]) / 448.f;
+        if (live) p.scales[row * p.n_blocks + b] = s;
+        bm[b] = __float_as_uint(s > 0.f ? 1.f / s : 1.f);
+      }
+      __syncthreads();
+    }
+    uint8_t* o8 = p.out8 + row * p.out8_stride;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = tx + i * TX;
-      if (live && e < H) atomicMax(&bm[e >> 7], abs_bits(t[i]));
+      if (tx + i * TX >= n) continue;
+      const float k = p.group ? __uint_as_float(bm[place(i) >> 7]) : inv;
+      if constexpr (VE == 1) o8[place(i)] = (uint8_t)e4m3x2(t[i][0] * k, 0.f);
+      else *reinterpret_cast<uint16_t*>(o8 + place(i)) = (uint16_t)e4m3x2(t[i][0] * k, t[i][1] * k);
     }
-    __syncthreads();
-    for (int b = tx; live && b < p.n_blocks; b += TX) p.scales[row * p.n_blocks + b] = __uint_as_float(bm[b]) / 448.f;
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = tx + i * TX;
-    if (!live || e >= H) continue;
-    const float s = __uint_as_float(p.group ? bm[e >> 7] : mx) / 448.f;
-    const float inv = s > 0.f ? 1.f / s : 1.f;  // zeros stay zeros; a NaN scale keeps its NaN values
-    p.out8[row * p.out8_stride + e] = (uint8_t)e4m3x2(t[i] * inv, 0.f);
+    if (p.group) __syncthreads();  // the next row's maxima take this one's place
   }
 }
 
@@ -426,23 +482,37 @@ cudaError_t launch_norm_staged(const NormParams& p, cudaStream_t s) {
                     dim3(tx), smem, s, p);
 }
 
-template <int DT, int NV>
+template <int DT, int VE, int TX, int NV, int MINB>
 cudaError_t launch_norm_any(const NormParams& p, cudaStream_t s) {
-  const int tx = ((p.H + NV - 1) / NV + 31) / 32 * 32;
-  const int ry = std::max(1, 256 / tx);
-  const size_t smem = p.out8 && p.group ? (size_t)ry * p.n_blocks * 4 : 0;
-  return launch_pdl(norm_any_kernel<DT, NV>, dim3((unsigned)((p.T + ry - 1) / ry)), dim3(tx, ry), smem, s, p);
+  constexpr int kRowsPerBlock = TX < 256 ? 256 / TX : 1;
+  const size_t smem = p.out8 && p.group ? (size_t)kRowsPerBlock * p.n_blocks * 4 : 0;
+  const int64_t blocks = ((int64_t)p.T + kRowsPerBlock - 1) / kRowsPerBlock;
+  return launch_pdl(norm_any_kernel<DT, VE, TX, NV, MINB>, dim3((unsigned)std::min(blocks, (int64_t)sm_count() * MINB)),
+                    dim3(TX, kRowsPerBlock), smem, s, p);
+}
+
+// Threads per row by the row's pieces: half or more of a thread's places are used. (H = 7169, T = 8192: 512 threads
+// with 16 pieces, two blocks per SM 209 us; 1024 with 8, one block 267, two 227; 512 with 16, three blocks, spills, 251.)
+template <int DT, int VE>
+cudaError_t norm_any_by_size(const NormParams& p, cudaStream_t s) {
+  const int n = p.H / VE;
+  if (n <= 256) return launch_norm_any<DT, VE, 32, 8, 6>(p, s);
+  if (n <= 1024) return launch_norm_any<DT, VE, 128, 8, 5>(p, s);
+  if (n <= 2048) return launch_norm_any<DT, VE, 256, 8, 5>(p, s);
+  if (n <= 4096) return launch_norm_any<DT, VE, 256, 16, 4>(p, s);
+  if (n <= 8192) return launch_norm_any<DT, VE, 512, 16, 2>(p, s);
+  if (VE == 2 || n <= 16384) return launch_norm_any<DT, VE, 1024, 16, 1>(p, s);
+  return launch_norm_any<DT, VE, 1024, VE == 2 ? 16 : 32, 1>(p, s);
 }
 
 template <int DT>
-cudaError_t norm_by_size(const NormParams& p, bool vec, cudaStream_t s) {
-  if (vec) {
+cudaError_t norm_by_size(const NormParams& p, int ve, cudaStream_t s) {
+  if (ve == 8) {
     if (p.H <= 1024) return launch_norm_rows<DT, 1, 128, 8>(p, s);
     if (p.H <= 8192) return launch_norm_staged<DT, 2, 512, 2>(p, s);
     if (p.H <= 14336) return launch_norm_staged<DT, 2, 896, 1>(p, s);
   }
-  if (p.H <= 4 * 1024) return launch_norm_any<DT, 4>(p, s);
-  return launch_norm_any<DT, 32>(p, s);
+  return ve == 1 ? norm_any_by_size<DT, 1>(p, s) : norm_any_by_size<DT, 2>(p, s);
 }
 
 // ---- a serving step's plan ---------------------------------------------------------------------
@@ -586,7 +656,7 @@ __device__ __forceinline__ float2 turned(uint64_t fraction, int pos, float mscal
 __device__ __forceinline__ bool cache_row(const moe_rotary_args& a, int p_shift, int slot, int64_t& kc, int64_t& vc) {
   const bool ok = slot >= 0 && slot < (a.num_pages << p_shift);
   if (slot < -1 || (slot >= 0 && !ok)) {
-    if (threadIdx.x == 0 && blockIdx.y == 0 && a.err) atomicOr(a.err, kErrIndex);
+    if (threadIdx.x == 0 && blockIdx.x == 0 && a.err) atomicOr(a.err, kErrIndex);
   }
   const int64_t page = slot >> p_shift, row = slot & (a.page_size - 1);
   kc = page * a.kc_page + row * a.kc_row;
@@ -594,40 +664,44 @@ __device__ __forceinline__ bool cache_row(const moe_rotary_args& a, int p_shift,
   return ok;
 }
 
-// 16-byte pieces. A token's work is the same list of items for every token: a rotated piece (in the half
+// Pieces of PE elements (8: 16 bytes). A token's work is the same list of items for every token: a rotated piece (in the half
 // layout with its partner half a rotary width away), a piece that passes, a piece of v. A thread
 // works out its U items once and then walks over tokens: all its loads first, then the token's
 // cosines and sines (shared by the heads; one exchange per token), then the products and stores.
+// Where a part of a head, a stride or an address is no multiple of 8 elements, the pieces are 4 or 1 elements.
 // Every element is read and written once, so memory bounds it: N = 8192, 96 + 2 x 8 heads of 128, bf16:
-// 72.0 us, 6.5 TB/s. U items per thread and blocks per SM measured there: 4 and 3 72.0, 4 and 4 (spills)
+// 72.0 us, 6.5 TB/s, and 93 in pieces of 4, 296 of 1; with 104 of 128 rotated in halves, which need pieces of 4, 107. U items per thread and blocks per SM measured there: 4 and 3 72.0, 4 and 4 (spills)
 // 87.5, 2 and 4 78.0, 2 and 6 77.4, 1 and 8 77.4 us; one item after another with two barriers per token 84 us.
-template <int DT, bool INTER, int U, int MINB>
+template <int DT, bool INTER, int PE, int U, int MINB>
 __global__ void __launch_bounds__(kRotaryThreads, MINB) rotary_kernel(const moe_rotary_args a, int p_shift) {
+  constexpr bool kInPiece = INTER && PE > 1;  // both elements of a pair lie in the piece
+  constexpr int kPairs = kInPiece ? PE / 2 : PE;
   // pair i sits at i + i / 8 * 2: pieces of 8 pairs are 80 bytes apart, so lanes on different pieces do not
   // meet in a bank
   __shared__ __align__(16) float2 cs[2][512 + 128];
   pdl_entry();
   const int tid = threadIdx.x, half = a.rot / 2;
-  const int r_pieces = INTER ? a.rot / 8 : half / 8, c_pieces = (a.D - a.rot) / 8, v_pieces = a.D / 8;
+  const int r_pieces = kInPiece ? a.rot / PE : half / PE, c_pieces = (a.D - a.rot) / PE, v_pieces = a.D / PE;
   const int h_pieces = r_pieces + c_pieces, heads = a.Hq + a.Hkv, n_rot = heads * h_pieces;
+  const int partner = INTER ? 1 : half;  // from a pair's first element to its second
   int64_t from[U], to[U];
   int kind[U], pair[U];  // kind: 0 nothing, 1 q, 2 k, 3 v; pair: the piece's first rotary pair, or -1
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int it = ((int)blockIdx.y * U + u) * kRotaryThreads + tid;
+    const int it = ((int)blockIdx.x * U + u) * kRotaryThreads + tid;
     kind[u] = 0;
     pair[u] = -1;
     from[u] = to[u] = 0;
     if (it < n_rot) {
       const int h = it / h_pieces;
-      int piece = it - h * h_pieces, at = piece * 8;
-      if (piece < r_pieces) pair[u] = INTER ? piece * 4 : piece * 8;
-      else at = a.rot + (piece - r_pieces) * 8;
+      int piece = it - h * h_pieces, at = piece * (INTER && PE == 1 ? 2 : PE);
+      if (piece < r_pieces) pair[u] = piece * kPairs;
+      else at = a.rot + (piece - r_pieces) * PE;
       kind[u] = h < a.Hq ? 1 : 2;
       from[u] = (h < a.Hq ? h * a.q_head : (h - a.Hq) * a.k_head) + at;
       to[u] = (h < a.Hq ? h * a.qo_head : (h - a.Hq) * a.kc_head) + at;
     } else if (it < n_rot + a.Hkv * v_pieces) {
-      const int j = it - n_rot, h = j / v_pieces, at = (j - h * v_pieces) * 8;
+      const int j = it - n_rot, h = j / v_pieces, at = (j - h * v_pieces) * PE;
       kind[u] = 3;
       from[u] = h * a.v_head + at;
       to[u] = h * a.vc_head + at;
@@ -635,20 +709,20 @@ __global__ void __launch_bounds__(kRotaryThreads, MINB) rotary_kernel(const moe_
   }
   const uint64_t f0 = tid < half ? turn_fraction(a.inv_freq[tid]) : 0;
   int turn = 0;
-  for (int n = blockIdx.x; n < a.N; n += gridDim.x, turn ^= 1) {
+  for (int n = blockIdx.y; n < a.N; n += gridDim.y, turn ^= 1) {
     int64_t kc, vc;
     const bool append = cache_row(a, p_shift, a.slots[n], kc, vc);
     const int pos = a.positions[n];
-    uint4 x[U], z[INTER ? 1 : U];
+    Piece<PE> x[U], z[kInPiece ? 1 : U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (kind[u] == 0 || (kind[u] > 1 && !append)) continue;
       const uint16_t* src = (kind[u] == 1   ? (const uint16_t*)a.q + n * a.q_tok
                              : kind[u] == 2 ? (const uint16_t*)a.k + n * a.k_tok
                                             : (const uint16_t*)a.v + n * a.v_tok) + from[u];
-      x[u] = *reinterpret_cast<const uint4*>(src);
-      if constexpr (!INTER)
-        if (pair[u] >= 0) z[u] = *reinterpret_cast<const uint4*>(src + half);
+      x[u] = *reinterpret_cast<const Piece<PE>*>(src);
+      if constexpr (!kInPiece)
+        if (pair[u] >= 0) z[u] = *reinterpret_cast<const Piece<PE>*>(src + partner);
     }
     for (int i = tid; i < half; i += kRotaryThreads)
       cs[turn][i + (i >> 3) * 2] = turned(i == tid ? f0 : turn_fraction(a.inv_freq[i]), pos, a.mscale);
@@ -660,101 +734,60 @@ __global__ void __launch_bounds__(kRotaryThreads, MINB) rotary_kernel(const moe_
                        : kind[u] == 2 ? (uint16_t*)a.k_cache + kc
                                       : (uint16_t*)a.v_cache + vc) + to[u];
       if (pair[u] < 0) {
-        *reinterpret_cast<uint4*>(dst) = x[u];
+        *reinterpret_cast<Piece<PE>*>(dst) = x[u];
         continue;
       }
-      const float2* c = cs[turn] + pair[u] + (pair[u] >> 3) * 2;
-      float p[8], y[8];
-      unpack8<DT>(x[u], p);
-      if constexpr (INTER) {
+      const float2* c = cs[turn] + pair[u] + (pair[u] >> 3) * 2;  // (a piece's pairs lie in one run of eight)
+      float p[PE], y[PE];
+      unpack<DT, PE>(x[u], p);
+      if constexpr (kInPiece) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < PE / 2; ++j) {
           y[2 * j] = p[2 * j] * c[j].x - p[2 * j + 1] * c[j].y;
           y[2 * j + 1] = p[2 * j] * c[j].y + p[2 * j + 1] * c[j].x;
         }
       } else {
-        float q[8], w[8];
-        unpack8<DT>(z[u], q);
+        float q[PE], w[PE];
+        unpack<DT, PE>(z[u], q);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < PE; ++j) {
           y[j] = p[j] * c[j].x - q[j] * c[j].y;
           w[j] = p[j] * c[j].y + q[j] * c[j].x;
         }
-        store_vec<DT, 8>(dst + half, w);
+        store_vec<DT, PE>(dst + partner, w);
       }
-      store_vec<DT, 8>(dst, y);
+      store_vec<DT, PE>(dst, y);
     }
   }
 }
 
-// One pair or element per item: any rotary width, stride and alignment.
-template <int DT, bool INTER>
-__global__ void __launch_bounds__(kRotaryThreads) rotary_any_kernel(const moe_rotary_args a, int p_shift) {
-  __shared__ float2 cs[512];
-  pdl_entry();
-  const int half = a.rot / 2, heads = a.Hq + a.Hkv, per_head = half + a.D - a.rot;
-  const int n_items = heads * per_head + a.Hkv * a.D;
-  for (int n = blockIdx.x; n < a.N; n += gridDim.x) {
-    for (int i = threadIdx.x; i < half; i += kRotaryThreads)
-      cs[i] = turned(turn_fraction(a.inv_freq[i]), a.positions[n], a.mscale);
-    int64_t kc, vc;
-    const bool append = cache_row(a, p_shift, a.slots[n], kc, vc);
-    __syncthreads();
-    for (int it = threadIdx.x; it < n_items; it += kRotaryThreads) {
-      const uint16_t* src;
-      uint16_t* dst;
-      int piece, h;
-      bool rotated = false;
-      if (it < heads * per_head) {
-        h = it / per_head;
-        piece = it - h * per_head;
-        rotated = piece < half;
-        if (!rotated) piece += a.rot - half;
-        src = h < a.Hq ? (const uint16_t*)a.q + n * a.q_tok + h * a.q_head
-                       : (const uint16_t*)a.k + n * a.k_tok + (h - a.Hq) * a.k_head;
-        dst = h < a.Hq ? (uint16_t*)a.q_out + n * a.qo_tok + h * a.qo_head
-                       : (uint16_t*)a.k_cache + kc + (h - a.Hq) * a.kc_head;
-        if (h >= a.Hq && !append) continue;
-      } else {
-        if (!append) continue;
-        const int j = it - heads * per_head;
-        h = j / a.D;
-        piece = j - h * a.D;
-        src = (const uint16_t*)a.v + n * a.v_tok + h * a.v_head;
-        dst = (uint16_t*)a.v_cache + vc + h * a.vc_head;
-      }
-      if (!rotated) {
-        dst[piece] = src[piece];
-      } else {
-        const int i0 = INTER ? 2 * piece : piece, i1 = INTER ? 2 * piece + 1 : piece + half;
-        const float x = to_f32<DT>(src[i0]), z = to_f32<DT>(src[i1]);
-        const float2 c = cs[piece];
-        dst[i0] = from_f32<DT>(x * c.x - z * c.y);
-        dst[i1] = from_f32<DT>(x * c.y + z * c.x);
-      }
-    }
-    __syncthreads();
-  }
+template <int DT, bool INTER, int PE, int U, int MINB>
+cudaError_t launch_rotary_as(const moe_rotary_args& a, int groups, int p_shift, cudaStream_t s) {
+  const int x = (groups + U - 1) / U;
+  const int y = std::max(1, std::min(a.N, MINB * sm_count() / x));
+  return launch_pdl(rotary_kernel<DT, INTER, PE, U, MINB>, dim3((unsigned)x, (unsigned)y), dim3(kRotaryThreads), 0, s, a, p_shift);
 }
 
-template <int DT, bool INTER, int U, int MINB>
-cudaError_t launch_rotary_vec(const moe_rotary_args& a, int groups, int p_shift, cudaStream_t s) {
-  const int y = (groups + U - 1) / U;
-  const int x = std::max(1, std::min(a.N, MINB * sm_count() / y));
-  return launch_pdl(rotary_kernel<DT, INTER, U, MINB>, dim3((unsigned)x, (unsigned)y), dim3(kRotaryThreads), 0, s, a, p_shift);
-}
-
-template <int DT, bool INTER>
-cudaError_t launch_rotary(const moe_rotary_args& a, bool vec, int p_shift, cudaStream_t s) {
-  if (!vec)
-    return launch_pdl(rotary_any_kernel<DT, INTER>, dim3((unsigned)std::min(a.N, 65535)), dim3(kRotaryThreads), 0, s, a,
-                      p_shift);
-  const int64_t items = (int64_t)(a.Hq + a.Hkv) * ((INTER ? a.rot : a.rot / 2) + a.D - a.rot) / 8 + (int64_t)a.Hkv * (a.D / 8);
+template <int DT, bool INTER, int PE>
+cudaError_t launch_rotary_pieces(const moe_rotary_args& a, int p_shift, cudaStream_t s) {
+  const int64_t rotated = INTER && PE > 1 ? a.rot / PE : a.rot / 2 / PE;  // pieces of a head
+  const int64_t items = (int64_t)(a.Hq + a.Hkv) * (rotated + (a.D - a.rot) / PE) + (int64_t)a.Hkv * (a.D / PE);
   const int groups = (int)((items + kRotaryThreads - 1) / kRotaryThreads);
-  // few tokens: a token's items over several blocks (N = 53: 2.6 us a launch in a graph against 3.6)
-  if (groups == 1 || (int64_t)a.N * groups <= 8 * sm_count()) return launch_rotary_vec<DT, INTER, 1, 8>(a, groups, p_shift, s);
-  if (groups == 2) return launch_rotary_vec<DT, INTER, 2, 6>(a, groups, p_shift, s);
-  return launch_rotary_vec<DT, INTER, 4, 3>(a, groups, p_shift, s);
+  // few tokens: a token's items over several blocks (N = 53: 2.6 us a launch in a graph against 3.6). Short pieces:
+  // the same, for more bytes in flight (N = 8192, 104 of 128 rotated in halves: 107 us against 129 with 4 items)
+  if constexpr (PE == 8) {
+    if (groups > 1 && (int64_t)a.N * groups > 8 * sm_count())
+      return groups == 2 ? launch_rotary_as<DT, INTER, PE, 2, 6>(a, groups, p_shift, s)
+                         : launch_rotary_as<DT, INTER, PE, 4, 3>(a, groups, p_shift, s);
+  }
+  return launch_rotary_as<DT, INTER, PE, 1, 8>(a, groups, p_shift, s);
+}
+
+template <int DT, bool INTER>
+cudaError_t launch_rotary(const moe_rotary_args& a, int pe, int p_shift, cudaStream_t s) {
+  return pe == 8   ? launch_rotary_pieces<DT, INTER, 8>(a, p_shift, s)
+         : pe == 4 ? launch_rotary_pieces<DT, INTER, 4>(a, p_shift, s)
+                   : launch_rotary_pieces<DT, INTER, 1>(a, p_shift, s);
 }
 
 int shift_of(int p) {
@@ -804,13 +837,16 @@ int moe_add_rmsnorm(void* stream, const moe_rmsnorm_args* a) {
   p.n_blocks = a->group ? (a->H + 127) / 128 : 1;
   p.eps = a->eps;
   p.err = a->err;
-  const auto ok16 = [](const void* q, int64_t stride) { return !q || (is_aligned(q, 16) && stride % 8 == 0); };
-  const bool vec = a->H % 8 == 0 && ok16(a->x, a->x_stride) && ok16(a->residual, a->residual_stride) &&
-                   ok16(a->out, a->out_stride) && ok16(a->residual_out, a->residual_out_stride) &&
-                   is_aligned(a->weight, 16) && (!a->out8 || (is_aligned(a->out8, 8) && a->out8_stride % 8 == 0));
+  // the widest piece that divides the width, the strides and the addresses: 8 elements, 2, or 1
+  const auto fits = [&](int n) {
+    const auto ok = [n](const void* q, int64_t stride, int size) { return !q || (is_aligned(q, n * size) && stride % n == 0); };
+    return a->H % n == 0 && ok(a->x, a->x_stride, 2) && ok(a->residual, a->residual_stride, 2) && ok(a->out, a->out_stride, 2) &&
+           ok(a->residual_out, a->residual_out_stride, 2) && ok(a->weight, 0, 2) && ok(a->out8, a->out8_stride, 1);
+  };
+  const int ve = fits(8) ? 8 : fits(2) ? 2 : 1;
   OpsPdl pdl;
-  const cudaError_t e = a->dtype == MOE_DT_BF16 ? norm_by_size<MOE_DT_BF16>(p, vec, (cudaStream_t)stream)
-                                                : norm_by_size<MOE_DT_F16>(p, vec, (cudaStream_t)stream);
+  const cudaError_t e = a->dtype == MOE_DT_BF16 ? norm_by_size<MOE_DT_BF16>(p, ve, (cudaStream_t)stream)
+                                                : norm_by_size<MOE_DT_F16>(p, ve, (cudaStream_t)stream);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -846,14 +882,20 @@ int moe_rotary_append(void* stream, const moe_rotary_args* a) {
   const void* t16[] = {a->q, a->k, a->v, a->q_out, a->k_cache, a->v_cache};
   const int64_t strides[] = {a->q_tok,  a->q_head,  a->k_tok,  a->k_head, a->v_tok,   a->v_head, a->qo_tok,
                              a->qo_head, a->kc_page, a->kc_row, a->kc_head, a->vc_page, a->vc_row, a->vc_head};
-  bool vec = a->D % 8 == 0 && a->rot % (a->interleaved ? 8 : 16) == 0;
+  // the widest piece that divides the head's parts, the strides and the addresses: 8 elements, 4, or 1
+  int pe = 8;
+  const auto fits = [&](int64_t v) {
+    if (v % pe) pe = v % 4 ? 1 : 4;
+  };
+  fits(a->D);
+  fits(a->interleaved ? a->rot : a->rot / 2);
   for (const void* p : t16) {
     if (!p || !is_aligned(p, 2)) return MOE_ERR_INVALID_ARG;
-    vec = vec && is_aligned(p, 16);
+    fits((int64_t)((uintptr_t)p / 2 % 8));
   }
   for (int64_t s : strides) {
     if (s < 0) return MOE_ERR_INVALID_ARG;
-    vec = vec && s % 8 == 0;
+    fits(s);
   }
   if (!a->positions || !a->slots || !a->inv_freq || !is_aligned(a->positions, 4) || !is_aligned(a->slots, 4) ||
       !is_aligned(a->inv_freq, 8) || !is_aligned(a->err, 4))
@@ -863,8 +905,8 @@ int moe_rotary_append(void* stream, const moe_rotary_args* a) {
   cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t e =
       a->dtype == MOE_DT_BF16
-          ? (a->interleaved ? launch_rotary<MOE_DT_BF16, true>(*a, vec, sh, st) : launch_rotary<MOE_DT_BF16, false>(*a, vec, sh, st))
-          : (a->interleaved ? launch_rotary<MOE_DT_F16, true>(*a, vec, sh, st) : launch_rotary<MOE_DT_F16, false>(*a, vec, sh, st));
+          ? (a->interleaved ? launch_rotary<MOE_DT_BF16, true>(*a, pe, sh, st) : launch_rotary<MOE_DT_BF16, false>(*a, pe, sh, st))
+          : (a->interleaved ? launch_rotary<MOE_DT_F16, true>(*a, pe, sh, st) : launch_rotary<MOE_DT_F16, false>(*a, pe, sh, st));
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -81,6 +81,14 @@ def test_norm_sizes(T, H, dtype, with_res, group, w32):
     check_norm(x, w, 1e-5, r, group, out, ro, o8, sc)
 
 
+@pytest.mark.parametrize("T,H,group", [(700, 258, 128), (401, 770, 0), (19, 1501, 128), (40, 2050, 128), (330, 3001, 0),
+                                       (310, 4098, 128), (309, 7170, 0), (33, 13001, 128), (160, 20002, 128),
+                                       (155, 20001, 0)])
+def test_norm_widths_not_of_eight(T, H, group):
+    """Pairs and single elements, every count of threads per row, more rows than blocks at work at once."""
+    test_norm_sizes(T, H, BF16, True, group, False)
+
+
 @pytest.mark.parametrize("H,off,pad", [(256, 0, 8), (256, 1, 3), (264, 8, 8), (250, 2, 6)])
 def test_norm_strides_and_in_place(H, off, pad):
     """Row views into wider buffers (aligned and not), residual updated in place, out over x;
@@ -263,6 +271,14 @@ def test_rotary_sizes(N, Hq, Hkv, D, rot, dtype, inter):
 def test_rotary_forms(kw):
     check_rotary(40, 6, 2, 64, 32, False, BF16, **kw)
     check_rotary(40, 6, 2, 64, 64, True, F16, **kw)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("N,Hq,Hkv,D,rot,pad", [(61, 12, 2, 64, 64, 4), (700, 6, 2, 128, 104, 0), (350, 24, 4, 68, 36, 0),
+                                                (600, 7, 1, 128, 128, 1), (45, 28, 4, 20, 10, 0)])
+def test_rotary_narrow_pieces(N, Hq, Hkv, D, rot, pad, inter):
+    """Rows, heads or rotated parts that are multiples of 4 elements, or of one, and not of 8."""
+    check_rotary(N, Hq, Hkv, D, rot, inter, BF16, pad=pad)
 
 
 def test_rotary_slots_out_of_range():
