@@ -13,8 +13,8 @@
 // as long as the keys it reads plus a constant for its start and end. Every CTA takes an
 // equal stretch of the axis, whatever mix of chunk lengths and contexts the call has; an item
 // that crosses a boundary is computed in pieces whose (m, l, O) go through the workspace, and
-// the CTA that finishes an item's last piece joins them in key order (so the result does not
-// depend on which one that was). The axis is laid out from the lengths by every CTA itself.
+// the CTA that finishes an item's last piece joins them in key order, many pieces in runs first (so the
+// result does not depend on which one that was). The axis is laid out from the lengths by every CTA itself.
 //
 // Warps. 0: TMA producer (Q, K and V tiles by page; a page that does not exist is an
 // out-of-range coordinate, which TMA fills with zeros). 1: issues the MMAs. 2, 3: clean V
@@ -32,12 +32,13 @@
 // up to one tile's tokens, or more.
 //   One row tile, 64 keys per step, two CTAs per SM: decoding and a few draft tokens stream the cache, so one
 //   CTA's softmax and items' ends hide behind the other's loads. 128 requests of 500 to 7,500 keys, 96 heads
-//   over 8 of 128, bf16: 318 to 326 us, 6.4 to 6.6 TB/s, bound by memory.
+//   over 8 of 128, bf16: 320 to 329 us, 6.4 to 6.6 TB/s, bound by memory (two row tiles: 341).
 //   Two row tiles, 128 keys per step, one CTA per SM: every K and V tile is used twice, and one tile's
 //   products run under the other's softmax. A chunk of 4,096 tokens over 16,384 keys, the same heads:
-//   1.89 ms, 1.53 PFLOP/s. Bound by the chain of a row tile's step: softmax 1,550 cycles (512 of them the
-//   exponentials' at 4 per instruction), handing over 200, and the MMAs after the last weights 1,040, of
-//   which each row tile's half overlaps the other's.
+//   1.76 ms in a short run, 1.88 to 1.92 ms under the power limit, 1.5 to 1.6 PFLOP/s (one row tile: 2.58). 32
+//   requests of 11 tokens, one more than a tile has, over 4,000 keys: 116 us against 183; of 10 107 and 111. Bound
+//   by the chain of a row tile's step: softmax 1,550 cycles (512 of them the exponentials' at 4 per instruction),
+//   handing over 200, and the MMAs after the last weights 1,040, of which each row tile's half overlaps the other's.
 // Measured on the way, same chunk: a thread chosen by lane number instead of elect.sync issues an MMA every 85
 // cycles instead of 45 (2.47 ms); a row split over two warps 2.28 ms (the exchange costs what the shorter
 // rows gain); one issuing thread per row tile 2.08 ms; waiting for the next tiles between the two row
@@ -69,10 +70,20 @@ namespace {
 
 constexpr int kRows = 128;          // rows of a tile (TMEM lanes)
 constexpr int kRuns = 128;          // runs of requests whose cost sums a CTA keeps
-constexpr int kMinStretch = 192;    // a CTA's least share of the axis (in keys): more CTAs than that are not worth a join
-constexpr int kWhole = 512;         // where a CTA's share is less than twice this, items up to this long are not split
+// A CTA's least share of the axis (in keys): more CTAs than that are not worth a join. One row tile: five requests
+// of up to 595 keys, 24 heads over 4 of 64: 128 11.2, 192 11.5, 256 13.3 us; one of 11,385 keys and 48 heads 30.9
+// with 128, 26.2 with 192. Two row tiles: three chunks of up to 1,147, two heads of 128: 192 32.1, 384 29.4, 512
+// 28.9 us; two chunks of 127 12.2, 15.7 and 12.0, and 17.9 with 768.
+template <int QT>
+constexpr int kMinStretch = QT == 1 ? 192 : 512;
+// Where a CTA's share is less than twice this, items up to this long are not split. Two row tiles: 27 chunks of 205
+// over 24 to 192 keys: 512 30.7, 896 23.9, 1280 23.8 us; one of 41 over 3,000 keys 18.1, 18.1 and 12.8; with 1792
+// four chunks of 2,729 take 69.5 us instead of 59.7. One row tile: 768 makes the five requests above 13.5 us.
+template <int QT>
+constexpr int kWhole = QT == 1 ? 512 : 1280;
 // What the start and end of an item of so many rows cost, in keys. With one row tile they hide behind the
-// other CTA of the SM; with two, O's way out and the join of a full tile cost as much as some keys.
+// other CTA of the SM; with two, O's way out and the join of a full tile cost as much as some keys. (28 decoding
+// requests and 5 prompts: a fixed 128 82.2, 384 77.9, 640 79.9, 256 and the rows 73.8, and twice the rows 76.2 us.)
 template <int QT>
 __device__ __forceinline__ int item_cost(int rows) { return QT == 1 ? 128 : 256 + rows; }
 constexpr int kNoteSlots = 8;       // pieces whose notes of non-finite tokens are kept (> V stages + 2)
@@ -86,8 +97,9 @@ struct AttnParams {
   int box_tok;     // tokens per Q box
   float scale_log2;
   uint32_t* err;
-  int32_t* tickets;  // [CTAs][QT] finished pieces of the split item that starts in the CTA; zero between calls
-  float* parts;      // [2 CTAs][QT] partial results: O [D/4][128][4], m [128], l [128]
+  int32_t* tickets;  // [CTAs][QT][3], zero between calls: finished pieces (or runs) of the split item that starts in
+                     // the CTA, of that item's first run, and of the run of an earlier item that starts in the CTA
+  float* parts;      // [2 CTAs][QT] partial results: O [D/4][128][4], m [128], l [128], m and l of a joined run
 };
 
 template <int DT_, int D_, int QT_, int BN_, int NK_, int NV_>
@@ -106,7 +118,7 @@ struct AttnCfg {
     return c;
   }
   static constexpr uint32_t kCols = cols();
-  static constexpr int kPart = kRows * (D + 2);  // floats of one partial result
+  static constexpr int kPart = kRows * (D + 4);  // floats of one partial result
   static_assert(NV + 2 < kNoteSlots, "notes of a piece outlive the pieces that can be loaded behind it");
 };
 
@@ -381,10 +393,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
   __syncthreads();
   Axis ax;
   ax.total = total;
-  ax.n = (int)max((int64_t)1, min((int64_t)gridDim.x, total / kMinStretch));
+  ax.n = (int)max((int64_t)1, min((int64_t)gridDim.x, total / kMinStretch<QT>));
   ax.each = div_floor(total, ax.n);
   ax.extra = (int)(total - ax.each * ax.n);
-  ax.whole = ax.each <= 2 * kWhole ? kWhole : 0;
+  ax.whole = ax.each <= 2 * kWhole<QT> ? kWhole<QT> : 0;
   ax.x0 = ax.x1 = 0;
   if (blockIdx.x < ax.n) {
     ax.x0 = ax.start(blockIdx.x);
@@ -822,43 +834,61 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         ++pn;
       }
       if (pc.split && n_tok > 0) {
-        __threadfence();
-        group_sync();
-        if (ok && r == 0) group_flag[q] = atomicAdd(&p.tickets[first * QT + q], 1) == pieces - 1;
-        group_sync();
-        if (!ok) break;
-        const bool join = *(volatile int*)&group_flag[q] != 0;
-        if (join) {
+        // Pieces are joined by the last to finish; many of them in two levels, runs of `fan` neighbours by each
+        // run's last, then the runs by the last run's: a join waits for one L2 access per few pieces. (One request of
+        // 60,000 keys, 96 heads over 8 of 128: 57 us, in one level 67; of 16,000 26.7 and 34; of 11,385 keys and four
+        // tokens, 48 heads over 4 of 64, 26 and 49. Up to 16 pieces one level: five of 6,000 keys 17.7 us, two 19.2.)
+        const int rows = n_tok * p.G, fan = pieces > 16 && pieces <= 64 ? 8 : 16;
+        bool whole = pieces <= fan;  // this join ends the item
+        int base = whole ? 0 : ((int)blockIdx.x - first) / fan * fan, step = 1;
+        int count = whole ? pieces : min(fan, pieces - base);
+        while (true) {
+          int32_t* ticket = p.tickets + ((first + base) * QT + q) * 3 + (whole ? 0 : base == 0 ? 1 : 2);
           __threadfence();
-          if (r == 0) p.tickets[first * QT + q] = 0;
-          const int rows = n_tok * p.G;
+          group_sync();
+          if (ok && r == 0) group_flag[q] = atomicAdd(ticket, 1) == count - 1;
+          group_sync();
+          if (!ok || *(volatile int*)&group_flag[q] == 0) break;
+          __threadfence();
+          if (r == 0) *ticket = 0;
           const auto piece_at = [&](int k) {
-            return p.parts + (size_t)((2 * (first + k) + (k == 0 ? 1 : 0)) * QT + q) * C::kPart;
+            const int x = base + k * step;
+            return p.parts + (size_t)((2 * (first + x) + (x == 0 ? 1 : 0)) * QT + q) * C::kPart;
           };
+          const int stat = kRows * (step > 1 ? D + 2 : D);  // where m and l are
+          float* run = piece_at(0);                         // where a run's result goes
           const auto row_out = [&](int row, int64_t& n, int& hd) {  // token and head of a row of the tile
             const int t = row / p.G;
             n = (int64_t)w.q0 + tok + t;
             hd = w.h * p.G + row - t * p.G;
           };
-          const auto row_lse = [&](float top, float sum) {
-            return sum == 0.f ? -INFINITY : (top * p.scale_log2 + log2f(sum)) * 0.69314718055994530942f;
+          const auto row_stat = [&](int row, float top, float sum) {
+            if (!whole) {
+              run[kRows * (D + 2) + row] = top;
+              run[kRows * (D + 3) + row] = sum;
+            } else if (p.a.lse) {
+              int64_t n;
+              int hd;
+              row_out(row, n, hd);
+              p.a.lse[n * p.a.Hq + hd] = sum == 0.f ? -INFINITY : (top * p.scale_log2 + log2f(sum)) * 0.69314718055994530942f;
+            }
           };
-          if (rows <= 32) {
-            // Few rows, perhaps many pieces (one long request): four columns of a row per thread, neighbours on
-            // neighbouring rows, eight pieces' loads at once.
-            constexpr int kAtOnce = 8;
+          // Two ways through the loads: four columns of a row per thread and eight pieces at once, or lane = row, each
+          // warp a quarter of the columns and two pieces at once. The one with fewer rounds.
+          constexpr int kAtOnce = 8;
+          if ((rows * (D / 4) + kRows - 1) / kRows * ((count + kAtOnce - 1) / kAtOnce) <= (rows + 31) / 32 * ((count + 1) / 2)) {
             for (int x = r; x < rows * (D / 4); x += kRows) {
-              const int c = x / rows, row = x - c * rows;
+              const int c = x / rows, row = x - c * rows;  // neighbours on neighbouring rows
               float top = -INFINITY, sum = 0.f;
               float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-              for (int k = 0; k < pieces; k += kAtOnce) {
+              for (int k = 0; k < count; k += kAtOnce) {
                 float mk[kAtOnce], lk[kAtOnce];
                 float4 o[kAtOnce];
 #pragma unroll
                 for (int u = 0; u < kAtOnce; ++u) {
-                  const float* pt = piece_at(min(k + u, pieces - 1));
-                  mk[u] = __ldcg(pt + kRows * D + row);
-                  lk[u] = k + u < pieces ? __ldcg(pt + kRows * (D + 1) + row) : 0.f;
+                  const float* pt = piece_at(min(k + u, count - 1));
+                  mk[u] = __ldcg(pt + stat + row);
+                  lk[u] = k + u < count ? __ldcg(pt + stat + kRows + row) : 0.f;
                   o[u] = __ldcg(reinterpret_cast<const float4*>(pt) + c * kRows + row);
                 }
 #pragma unroll
@@ -874,66 +904,82 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
                   acc.w = acc.w * f0 + o[u].w * f;
                 }
               }
+              if (c == 0) row_stat(row, top, sum);
+              if (!whole) {
+                reinterpret_cast<float4*>(run)[c * kRows + row] = acc;
+                continue;
+              }
               const float inv = sum == 0.f ? 0.f : 1.f / sum;
               int64_t n;
               int hd;
               row_out(row, n, hd);
               *reinterpret_cast<uint2*>((uint16_t*)p.a.out + n * p.a.out_tok + (int64_t)hd * p.a.out_head + 4 * c) =
                   make_uint2(pack2<DT>(acc.x * inv, acc.y * inv), pack2<DT>(acc.z * inv, acc.w * inv));
-              if (p.a.lse && c == 0) p.a.lse[n * p.a.Hq + hd] = row_lse(top, sum);
             }
-          } else
-          // Lane = row, each warp a quarter of the columns, two pieces at a time.
-          for (int r0 = 0; r0 < rows; r0 += 32) {
-            constexpr int kCols4 = D / 16;
-            const int row = min(r0 + lane, rows - 1);
-            float top = -INFINITY, sum = 0.f;
-            float4 acc[kCols4];
+          } else {
+            for (int r0 = 0; r0 < rows; r0 += 32) {
+              constexpr int kCols4 = D / 16;
+              const int row = min(r0 + lane, rows - 1);
+              float top = -INFINITY, sum = 0.f;
+              float4 acc[kCols4];
 #pragma unroll
-            for (int j = 0; j < kCols4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = 0; k < pieces; k += 2) {
-              float mk[2], lk[2];
-              float4 o[2][kCols4];
+              for (int j = 0; j < kCols4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+              for (int k = 0; k < count; k += 2) {
+                float mk[2], lk[2];
+                float4 o[2][kCols4];
 #pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const float* pt = piece_at(min(k + u, pieces - 1));
-                mk[u] = __ldcg(pt + kRows * D + row);
-                lk[u] = k + u < pieces ? __ldcg(pt + kRows * (D + 1) + row) : 0.f;
+                for (int u = 0; u < 2; ++u) {
+                  const float* pt = piece_at(min(k + u, count - 1));
+                  mk[u] = __ldcg(pt + stat + row);
+                  lk[u] = k + u < count ? __ldcg(pt + stat + kRows + row) : 0.f;
 #pragma unroll
-                for (int j = 0; j < kCols4; ++j)
-                  o[u][j] = __ldcg(reinterpret_cast<const float4*>(pt) + (quarter * kCols4 + j) * kRows + row);
-              }
+                  for (int j = 0; j < kCols4; ++j)
+                    o[u][j] = __ldcg(reinterpret_cast<const float4*>(pt) + (quarter * kCols4 + j) * kRows + row);
+                }
 #pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                if (lk[u] == 0.f) continue;  // the row saw nothing in this piece; its O may not be written
-                const float nt = fmaxf(top, mk[u]);
-                const float f0 = ex2((top - nt) * p.scale_log2), f = ex2((mk[u] - nt) * p.scale_log2);
-                top = nt;
-                sum = sum * f0 + lk[u] * f;
+                for (int u = 0; u < 2; ++u) {
+                  if (lk[u] == 0.f) continue;  // the row saw nothing in this piece; its O may not be written
+                  const float nt = fmaxf(top, mk[u]);
+                  const float f0 = ex2((top - nt) * p.scale_log2), f = ex2((mk[u] - nt) * p.scale_log2);
+                  top = nt;
+                  sum = sum * f0 + lk[u] * f;
 #pragma unroll
-                for (int j = 0; j < kCols4; ++j) {
-                  acc[j].x = acc[j].x * f0 + o[u][j].x * f;
-                  acc[j].y = acc[j].y * f0 + o[u][j].y * f;
-                  acc[j].z = acc[j].z * f0 + o[u][j].z * f;
-                  acc[j].w = acc[j].w * f0 + o[u][j].w * f;
+                  for (int j = 0; j < kCols4; ++j) {
+                    acc[j].x = acc[j].x * f0 + o[u][j].x * f;
+                    acc[j].y = acc[j].y * f0 + o[u][j].y * f;
+                    acc[j].z = acc[j].z * f0 + o[u][j].z * f;
+                    acc[j].w = acc[j].w * f0 + o[u][j].w * f;
+                  }
                 }
               }
-            }
-            if (r0 + lane >= rows) continue;
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            int64_t n;
-            int hd;
-            row_out(row, n, hd);
-            uint16_t* out = (uint16_t*)p.a.out + n * p.a.out_tok + (int64_t)hd * p.a.out_head + quarter * (D / 4);
+              __syncwarp();  // lanes past the last row have read its values, which it may now replace
+              if (r0 + lane >= rows) continue;
+              if (quarter == 0) row_stat(row, top, sum);
+              if (!whole) {
 #pragma unroll
-            for (int j = 0; j < kCols4; j += 2)
-              *reinterpret_cast<uint4*>(out + 4 * j) =
-                  make_uint4(pack2<DT>(acc[j].x * inv, acc[j].y * inv), pack2<DT>(acc[j].z * inv, acc[j].w * inv),
-                             pack2<DT>(acc[j + 1].x * inv, acc[j + 1].y * inv),
-                             pack2<DT>(acc[j + 1].z * inv, acc[j + 1].w * inv));
-            if (p.a.lse && quarter == 0) p.a.lse[n * p.a.Hq + hd] = row_lse(top, sum);
+                for (int j = 0; j < kCols4; ++j) reinterpret_cast<float4*>(run)[(quarter * kCols4 + j) * kRows + row] = acc[j];
+                continue;
+              }
+              const float inv = sum == 0.f ? 0.f : 1.f / sum;
+              int64_t n;
+              int hd;
+              row_out(row, n, hd);
+              uint16_t* out = (uint16_t*)p.a.out + n * p.a.out_tok + (int64_t)hd * p.a.out_head + quarter * (D / 4);
+#pragma unroll
+              for (int j = 0; j < kCols4; j += 2)
+                *reinterpret_cast<uint4*>(out + 4 * j) =
+                    make_uint4(pack2<DT>(acc[j].x * inv, acc[j].y * inv), pack2<DT>(acc[j].z * inv, acc[j].w * inv),
+                               pack2<DT>(acc[j + 1].x * inv, acc[j + 1].y * inv),
+                               pack2<DT>(acc[j + 1].z * inv, acc[j + 1].w * inv));
+            }
           }
+          if (whole) break;
+          whole = true;
+          count = (pieces + fan - 1) / fan;
+          step = fan;
+          base = 0;
         }
+        if (!ok) break;
       }
       w = *place;
       ax = *parked_axis;
@@ -1069,9 +1115,9 @@ int moe_attn_create(int device, moe_attn_ctx** out) {
   if (!c) return MOE_ERR_OOM;
   c->device = device;
   c->sm_count = prop.multiProcessorCount;
-  // error word | tickets (one per CTA and row tile) | partial results (two per CTA and row tile)
+  // error word | tickets (three per CTA and row tile) | partial results (two per CTA and row tile)
   const size_t most = 2 * (size_t)c->sm_count;
-  const size_t head = (256 + most * 4 + 255) / 256 * 256;
+  const size_t head = (256 + most * 3 * 4 + 255) / 256 * 256;
   c->head_bytes = head;
   c->bytes = head + 2 * most * sizeof(float) * StreamCfg<0, 128>::kPart;
   if (cudaMalloc(&c->mem, c->bytes) != cudaSuccess) {

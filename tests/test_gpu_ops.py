@@ -404,6 +404,17 @@ def test_attention_long(handle, D, Hq, Hkv, ctx, new, every):
     check_attention(handle, c, max_new=max(new), every=every)
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,ctx,new,P", [
+    (64, 1, 1, [1700], [1], 16), (64, 48, 4, [11385], [4], 128), (128, 6, 1, [12315], [1], 64),
+    (128, 100, 1, [17000], [1], 32), (128, 12, 2, [9000, 400], [10, 2], 64), (64, 2, 1, [40000], [2], 64),
+    (128, 2, 1, [5000], [118], 64), (64, 32, 1, [2500, 16000], [3, 9], 64)])
+def test_attention_many_pieces(handle, D, Hq, Hkv, ctx, new, P):
+    """Few items on many CTAs: runs of pieces joined first, then the runs, with few and with many rows."""
+    c = a_cache(len(ctx) + D + P, ctx, new, Hq, Hkv, D, P, BF16)
+    check_attention(handle, c, every=3 if max(new) > 20 else 1)
+    check_attention(handle, c, max_new=max(new), every=3 if max(new) > 20 else 1)
+
+
 def test_attention_rows_without_keys(handle):
     """kv_lens below the number of new tokens leaves the first rows nothing to see: zeros and
     a log-sum of -inf; with no key at all every row is empty."""
