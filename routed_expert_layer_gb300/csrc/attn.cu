@@ -71,7 +71,7 @@ namespace {
 constexpr int kRows = 128;          // rows of a tile (TMEM lanes)
 constexpr int kRuns = 128;          // runs of requests whose cost sums a CTA keeps
 // A CTA's least share of the axis (in keys): more CTAs than that are not worth a join. One row tile: five requests
-// of up to 595 keys, 24 heads over 4 of 64: 128 11.2, 192 11.5, 256 13.3 us; one of 11,385 keys and 48 heads 30.9
+// of up to 595 keys, 24 heads over 4 of 64: 128 11.2, 192 11.1 to 11.5, 256 13.3 us; one of 11,385 keys and 48 heads 30.9
 // with 128, 26.2 with 192. Two row tiles: three chunks of up to 1,147, two heads of 128: 192 32.1, 384 29.4, 512
 // 28.9 us; two chunks of 127 12.2, 15.7 and 12.0, and 17.9 with 768.
 template <int QT>
@@ -81,11 +81,12 @@ constexpr int kMinStretch = QT == 1 ? 192 : 512;
 // four chunks of 2,729 take 69.5 us instead of 59.7. One row tile: 768 makes the five requests above 13.5 us.
 template <int QT>
 constexpr int kWhole = QT == 1 ? 512 : 1280;
-// What the start and end of an item of so many rows cost, in keys. With one row tile they hide behind the
-// other CTA of the SM; with two, O's way out and the join of a full tile cost as much as some keys. (28 decoding
+// What the start and end of an item of so many rows cost, in keys. With one row tile they partly hide behind the
+// other CTA of the SM (49 requests of 211 to 1,693 keys, 12 heads over 2 of 128: 128 23.5, 176 21.6, 224 21.2,
+// 384 21.7 us; the five requests above 11.5, 11.1, 11.6, 11.9; eight of 52 to 417 12.3, 13.5, 13.6, 14.4); with two, O's way out and the join of a full tile cost as much as some keys. (28 decoding
 // requests and 5 prompts: a fixed 128 82.2, 384 77.9, 640 79.9, 256 and the rows 73.8, and twice the rows 76.2 us.)
 template <int QT>
-__device__ __forceinline__ int item_cost(int rows) { return QT == 1 ? 128 : 256 + rows; }
+__device__ __forceinline__ int item_cost(int rows) { return QT == 1 ? 176 : 256 + rows; }
 constexpr int kNoteSlots = 8;       // pieces whose notes of non-finite tokens are kept (> V stages + 2)
 constexpr float kRescaleLog2 = 8.f;
 
@@ -420,28 +421,6 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
     while (more) {
       const Piece<QT, BN> pc(p, w, ax);
       if (pc.tiles()) {
-        if (!warp_wait(qempty, (qn & 1) ^ 1u, p.err)) {
-          ok = false;
-          break;
-        }
-        ++qn;
-        if (lane == 0) {
-          const int box_bytes = p.box_tok * p.G * 128;
-          int boxes[QT], n = 0;
-#pragma unroll
-          for (int q = 0; q < QT; ++q) {
-            const int tok = (w.i * QT + q) * p.tpt;
-            boxes[q] = pc.tq1[q] > pc.t0 ? (min(p.tpt, w.n_new - tok) + p.box_tok - 1) / p.box_tok : 0;
-            n += boxes[q];
-          }
-          mbar_arrive_expect_tx(qfull, (uint32_t)(n * (D / 64) * box_bytes));
-          for (int q = 0; q < QT; ++q)
-            for (int x = 0; x < boxes[q]; ++x)
-              for (int d = 0; d < D / 64; ++d)
-                tma_3d(sq + q * C::kQ + d * C::kQBlk + x * box_bytes, &map_q, d * 64, w.h * p.G,
-                       w.q0 + (w.i * QT + q) * p.tpt + x * p.box_tok, qfull);
-        }
-        __syncwarp();
         const int32_t* table = p.a.block_table + w.b * p.a.table_stride;
         // pages are looked up 32 at a time, the next 32 while these are copied
         const auto inside = [&](int col) { return ((int64_t)col << p.p_shift) < pc.kv_end; };  // (the table holds kv_end)
@@ -474,6 +453,29 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
             for (int d = 0; d < D / 64; ++d)
               tma_4d(sk + ks * C::kTile + d * C::kBlk + lane * rows * 128, &map_k, d * 64, row, w.h, id, &kfull[ks]);
           ++kn;
+          if (t == pc.t0) {
+            // Q behind the first K tile: its place is free only after the last item's S, K's may be before that
+            ok = warp_wait(qempty, (qn & 1) ^ 1u, p.err);
+            if (!ok) break;
+            ++qn;
+            if (lane == 0) {
+              const int box_bytes = p.box_tok * p.G * 128;
+              int boxes[QT], n = 0;
+#pragma unroll
+              for (int q = 0; q < QT; ++q) {
+                const int tok = (w.i * QT + q) * p.tpt;
+                boxes[q] = pc.tq1[q] > pc.t0 ? (min(p.tpt, w.n_new - tok) + p.box_tok - 1) / p.box_tok : 0;
+                n += boxes[q];
+              }
+              mbar_arrive_expect_tx(qfull, (uint32_t)(n * (D / 64) * box_bytes));
+              for (int q = 0; q < QT; ++q)
+                for (int x = 0; x < boxes[q]; ++x)
+                  for (int d = 0; d < D / 64; ++d)
+                    tma_3d(sq + q * C::kQ + d * C::kQBlk + x * box_bytes, &map_q, d * 64, w.h * p.G,
+                           w.q0 + (w.i * QT + q) * p.tpt + x * p.box_tok, qfull);
+            }
+            __syncwarp();
+          }
           ok = warp_wait(&vempty[vs], ((vn / NV) & 1) ^ 1u, p.err);
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&vfull[vs], C::kTile);
