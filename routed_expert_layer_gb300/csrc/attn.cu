@@ -71,9 +71,9 @@ namespace {
 constexpr int kRows = 128;          // rows of a tile (TMEM lanes)
 constexpr int kRuns = 128;          // runs of requests whose cost sums a CTA keeps
 // A CTA's least share of the axis (in keys): more CTAs than that are not worth a join. One row tile: five requests
-// of up to 595 keys, 24 heads over 4 of 64: 128 11.2, 192 11.1 to 11.5, 256 13.3 us; one of 11,385 keys and 48 heads 30.9
-// with 128, 26.2 with 192. Two row tiles: three chunks of up to 1,147, two heads of 128: 192 32.1, 384 29.4, 512
-// 28.9 us; two chunks of 127 12.2, 15.7 and 12.0, and 17.9 with 768.
+// of up to 595 keys, 24 heads over 4 of 64: 128 11.2, 192 11.1 to 11.5, 256 13.3 us; one of 11,385 keys and 48
+// heads 30.9 with 128, 26.2 with 192. Two row tiles: three chunks of up to 1,147, two heads of 128: 192 32.1,
+// 384 29.4, 512 28.9 us; two chunks of 127 12.2, 15.7 and 12.0, and 17.9 with 768.
 template <int QT>
 constexpr int kMinStretch = QT == 1 ? 192 : 512;
 // Where a CTA's share is less than twice this, items up to this long are not split. Two row tiles: 27 chunks of 205
@@ -82,9 +82,10 @@ constexpr int kMinStretch = QT == 1 ? 192 : 512;
 template <int QT>
 constexpr int kWhole = QT == 1 ? 512 : 1280;
 // What the start and end of an item of so many rows cost, in keys. With one row tile they partly hide behind the
-// other CTA of the SM (49 requests of 211 to 1,693 keys, 12 heads over 2 of 128: 128 23.5, 176 21.6, 224 21.2,
-// 384 21.7 us; the five requests above 11.5, 11.1, 11.6, 11.9; eight of 52 to 417 12.3, 13.5, 13.6, 14.4); with two, O's way out and the join of a full tile cost as much as some keys. (28 decoding
-// requests and 5 prompts: a fixed 128 82.2, 384 77.9, 640 79.9, 256 and the rows 73.8, and twice the rows 76.2 us.)
+// other CTA of the SM: 49 requests of 211 to 1,693 keys, 12 heads over 2 of 128: 128 23.5, 176 21.6, 224 21.2,
+// 384 21.7 us; the five requests above 11.5, 11.1, 11.6, 11.9; eight of 52 to 417 12.3, 13.5, 13.6, 14.4. With two,
+// O's way out and the join of a full tile cost as much as some keys: 28 decoding requests and 5 prompts: a fixed
+// 128 82.2, 384 77.9, 640 79.9, 256 and the rows 73.8, and twice the rows 76.2 us.
 template <int QT>
 __device__ __forceinline__ int item_cost(int rows) { return QT == 1 ? 176 : 256 + rows; }
 constexpr int kNoteSlots = 8;       // pieces whose notes of non-finite tokens are kept (> V stages + 2)
