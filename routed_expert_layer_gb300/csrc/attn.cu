@@ -422,6 +422,28 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
     while (more) {
       const Piece<QT, BN> pc(p, w, ax);
       if (pc.tiles()) {
+        if (!warp_wait(qempty, (qn & 1) ^ 1u, p.err)) {
+          ok = false;
+          break;
+        }
+        ++qn;
+        if (lane == 0) {
+          const int box_bytes = p.box_tok * p.G * 128;
+          int boxes[QT], n = 0;
+#pragma unroll
+          for (int q = 0; q < QT; ++q) {
+            const int tok = (w.i * QT + q) * p.tpt;
+            boxes[q] = pc.tq1[q] > pc.t0 ? (min(p.tpt, w.n_new - tok) + p.box_tok - 1) / p.box_tok : 0;
+            n += boxes[q];
+          }
+          mbar_arrive_expect_tx(qfull, (uint32_t)(n * (D / 64) * box_bytes));
+          for (int q = 0; q < QT; ++q)
+            for (int x = 0; x < boxes[q]; ++x)
+              for (int d = 0; d < D / 64; ++d)
+                tma_3d(sq + q * C::kQ + d * C::kQBlk + x * box_bytes, &map_q, d * 64, w.h * p.G,
+                       w.q0 + (w.i * QT + q) * p.tpt + x * p.box_tok, qfull);
+        }
+        __syncwarp();
         const int32_t* table = p.a.block_table + w.b * p.a.table_stride;
         // pages are looked up 32 at a time, the next 32 while these are copied
         const auto inside = [&](int col) { return ((int64_t)col << p.p_shift) < pc.kv_end; };  // (the table holds kv_end)
@@ -454,29 +476,6 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
             for (int d = 0; d < D / 64; ++d)
               tma_4d(sk + ks * C::kTile + d * C::kBlk + lane * rows * 128, &map_k, d * 64, row, w.h, id, &kfull[ks]);
           ++kn;
-          if (t == pc.t0) {
-            // Q behind the first K tile: its place is free only after the last item's S, K's may be before that
-            ok = warp_wait(qempty, (qn & 1) ^ 1u, p.err);
-            if (!ok) break;
-            ++qn;
-            if (lane == 0) {
-              const int box_bytes = p.box_tok * p.G * 128;
-              int boxes[QT], n = 0;
-#pragma unroll
-              for (int q = 0; q < QT; ++q) {
-                const int tok = (w.i * QT + q) * p.tpt;
-                boxes[q] = pc.tq1[q] > pc.t0 ? (min(p.tpt, w.n_new - tok) + p.box_tok - 1) / p.box_tok : 0;
-                n += boxes[q];
-              }
-              mbar_arrive_expect_tx(qfull, (uint32_t)(n * (D / 64) * box_bytes));
-              for (int q = 0; q < QT; ++q)
-                for (int x = 0; x < boxes[q]; ++x)
-                  for (int d = 0; d < D / 64; ++d)
-                    tma_3d(sq + q * C::kQ + d * C::kQBlk + x * box_bytes, &map_q, d * 64, w.h * p.G,
-                           w.q0 + (w.i * QT + q) * p.tpt + x * p.box_tok, qfull);
-            }
-            __syncwarp();
-          }
           ok = warp_wait(&vempty[vs], ((vn / NV) & 1) ^ 1u, p.err);
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&vfull[vs], C::kTile);
