@@ -32,10 +32,10 @@
 // up to one tile's tokens, or more.
 //   One row tile, 64 keys per step, two CTAs per SM: decoding and a few draft tokens stream the cache, so one
 //   CTA's softmax and items' ends hide behind the other's loads. 128 requests of 500 to 7,500 keys, 96 heads
-//   over 8 of 128, bf16: 320 to 329 us, 6.4 to 6.6 TB/s, bound by memory (two row tiles: 341).
+//   over 8 of 128, bf16: 315 to 329 us, 6.4 to 6.6 TB/s, bound by memory (two row tiles: 341).
 //   Two row tiles, 128 keys per step, one CTA per SM: every K and V tile is used twice, and one tile's
 //   products run under the other's softmax. A chunk of 4,096 tokens over 16,384 keys, the same heads:
-//   1.76 ms in a short run, 1.88 to 1.92 ms under the power limit, 1.5 to 1.6 PFLOP/s (one row tile: 2.58). 32
+//   1.76 ms in a short run, 1.88 to 1.99 ms under the power limit, 1.45 to 1.64 PFLOP/s (one row tile: 2.58). 32
 //   requests of 11 tokens, one more than a tile has, over 4,000 keys: 116 us against 183; of 10 107 and 111. Bound
 //   by the chain of a row tile's step: softmax 1,550 cycles (512 of them the exponentials' at 4 per instruction),
 //   handing over 200, and the MMAs after the last weights 1,040, of which each row tile's half overlaps the other's.
