@@ -37,7 +37,8 @@ extern "C" {
  *   y = t / sqrt(mean(t^2) + eps) * weight (fp32)      out = round(y)
  *   out8 = e4m3(y / s) rounded to nearest even, s = max|y| / 448 over the row (group 0) or
  *   over each `group` = 128 consecutive elements (the last block may be shorter); s in
- *   scales[row][block]. A block of zeros has s = 0 and zeros in out8.
+ *   scales[row][block]. A block of zeros has s = 0 and zeros in out8, and so has one whose values are
+ *   at most 448 * 2^-150, for which s rounds to 0.
  * x, residual, out, residual_out [T][H] with row strides; weight [H] in dtype, or fp32 with
  * weight_f32 = 1. residual_out may be residual itself (in place) and out may be x itself;
  * no other overlap. out or out8 may be NULL (not both); scales goes with out8.

@@ -70,6 +70,11 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 // |v| as an unsigned integer: its order is that of the magnitudes, and a NaN is the largest.
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
+// The 8-bit output is y / s as y * (1 / s). Where s lies below fp32's normal range, 1 / s lies above its largest
+// value: there both y and s are taken kLift times larger first.
+constexpr float kLift = 0x1p64f;
+__device__ __forceinline__ bool needs_lift(float s) { return s > 0.f && s < 0x1p-126f; }
+
 // Reductions over the warps of one row (block row threadIdx.y); red has one word per warp.
 __device__ __forceinline__ float row_sum(float v, float* red) {
 #pragma unroll
@@ -118,7 +123,7 @@ __device__ __forceinline__ uint4 load16(const uint16_t* p) { return __ldg(reinte
 
 // The 8-bit output and scales of a row whose chunks are in t (|t| up to mx in this thread), by the whole block.
 template <int NV>
-__device__ __forceinline__ void write_8bit(const NormParams& p, int64_t row, bool live, const float (&t)[NV][8],
+__device__ __forceinline__ void write_8bit(const NormParams& p, int64_t row, bool live, float (&t)[NV][8],
                                            uint32_t mx, uint32_t* red) {
   const int tx = threadIdx.x, TX = blockDim.x, H = p.H;
   if (p.group == 0) {
@@ -139,7 +144,12 @@ __device__ __forceinline__ void write_8bit(const NormParams& p, int64_t row, boo
       if (live && e < H && (tx & 15) == 0) p.scales[row * p.n_blocks + (e >> 7)] = __uint_as_float(m) / 448.f;
     }
     if (!live || e >= H) continue;
-    const float s = __uint_as_float(m) / 448.f;
+    float s = __uint_as_float(m) / 448.f;
+    if (needs_lift(s)) {
+      s *= kLift;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[i][j] *= kLift;
+    }
     const float inv = s > 0.f ? 1.f / s : 1.f;  // zeros stay zeros; a NaN scale keeps its NaN values
     uint2 q;
     q.x = e4m3x2(t[i][0] * inv, t[i][1] * inv) | e4m3x2(t[i][2] * inv, t[i][3] * inv) << 16;
@@ -407,6 +417,13 @@ __global__ void __launch_bounds__(TX < 256 ? 256 : TX, MINB) norm_any_kernel(con
       const float s = __uint_as_float(row_max(mx, red_max[turn])) / 448.f;
       if (live && tx == 0) p.scales[row] = s;
       inv = s > 0.f ? 1.f / s : 1.f;  // zeros stay zeros; a NaN scale keeps its NaN values
+      if (needs_lift(s)) {
+        inv = 1.f / (s * kLift);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int j = 0; j < VE; ++j) t[i][j] *= kLift;
+      }
     } else {
       for (int b = tx; b < p.n_blocks; b += TX) bm[b] = 0;
       __syncthreads();
@@ -422,7 +439,8 @@ __global__ void __launch_bounds__(TX < 256 ? 256 : TX, MINB) norm_any_kernel(con
       for (int b = tx; b < p.n_blocks; b += TX) {
         const float s = __uint_as_float(bm[b]) / 448.f;
         if (live) p.scales[row * p.n_blocks + b] = s;
-        bm[b] = __float_as_uint(s > 0.f ? 1.f / s : 1.f);
+        // negative: the block's values are lifted
+        bm[b] = __float_as_uint(needs_lift(s) ? -1.f / (s * kLift) : s > 0.f ? 1.f / s : 1.f);
       }
       __syncthreads();
     }
@@ -430,7 +448,13 @@ __global__ void __launch_bounds__(TX < 256 ? 256 : TX, MINB) norm_any_kernel(con
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (tx + i * TX >= n) continue;
-      const float k = p.group ? __uint_as_float(bm[place(i) >> 7]) : inv;
+      float k = inv;
+      if (p.group) {
+        k = __uint_as_float(bm[place(i) >> 7]);
+        if (k < 0.f)
+#pragma unroll
+          for (int j = 0; j < VE; ++j) t[i][j] *= -kLift;
+      }
       if constexpr (VE == 1) o8[place(i)] = (uint8_t)e4m3x2(t[i][0] * k, 0.f);
       else *reinterpret_cast<uint16_t*>(o8 + place(i)) = (uint16_t)e4m3x2(t[i][0] * k, t[i][1] * k);
     }
