@@ -26,7 +26,10 @@
 // most 2^8, which neither the fp32 sums nor P's 16-bit floating point notice.
 //
 // P is rounded to the type of the cache for the second product (the tensor cores take no
-// other); l sums the unrounded values.
+// other); l sums the unrounded values. f16 ends 2^-24 below 1, where the many small weights of a long
+// context beside one large one would vanish from O and not from l: there P is taken 2^7 times larger, so that
+// the largest, 2^8 of the lazy maximum included, is 2^15 and what is lost lies below 2^-32 of a row's
+// largest weight. O and l carry the factor alike; only the logarithm of l has to shed it.
 //
 // Two instances per head width, chosen by the most rows a request can have (max_new, or all of N):
 // up to one tile's tokens, or more.
@@ -90,6 +93,8 @@ template <int QT>
 __device__ __forceinline__ int item_cost(int rows) { return QT == 1 ? 176 : 256 + rows; }
 constexpr int kNoteSlots = 8;       // pieces whose notes of non-finite tokens are kept (> V stages + 2)
 constexpr float kRescaleLog2 = 8.f;
+template <int DT>
+constexpr float kLiftLog2 = DT == MOE_DT_F16 ? 7.f : 0.f;  // P and l are 2^kLiftLog2 times the weights (bf16 has fp32's range)
 
 struct AttnParams {
   moe_attn_args a;
@@ -295,6 +300,12 @@ __device__ __forceinline__ void exp32(uint32_t* v, float2 scale, float2 off, flo
     sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], e);
     v[k / 2] = pack2<DT>(e.x, e.y);
   }
+}
+
+// ln of a row's sum of exp(scale * score), from its maximum and its sum of weights.
+template <int DT>
+__device__ __forceinline__ float log_sum(float m, float l, float scale_log2) {
+  return l == 0.f ? -INFINITY : (m * scale_log2 + (log2f(l) - kLiftLog2<DT>)) * 0.69314718055994530942f;
 }
 
 template <int DT>
@@ -725,7 +736,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
               for (int c = 0; c < BN; c += 32) tmem_wait_ld32(s + c);
             }
           }
-          const float off = m == -INFINITY ? 0.f : -m * p.scale_log2;
+          const float off = m == -INFINITY ? 0.f : fmaf(-m, p.scale_log2, kLiftLog2<DT>);
           float2 sum[2] = {};
 #pragma unroll
           for (int half = 0; half < 2; ++half) {  // the MMAs can start on the first half of the weights
@@ -824,8 +835,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
             part[kRows * D + r] = m;
             part[kRows * (D + 1) + r] = l;
           } else if (p.a.lse) {
-            p.a.lse[n_row * p.a.Hq + head] =
-                l == 0.f ? -INFINITY : (m * p.scale_log2 + log2f(l)) * 0.69314718055994530942f;
+            p.a.lse[n_row * p.a.Hq + head] = log_sum<DT>(m, l, p.scale_log2);
           }
         }
       }
@@ -872,7 +882,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
               int64_t n;
               int hd;
               row_out(row, n, hd);
-              p.a.lse[n * p.a.Hq + hd] = sum == 0.f ? -INFINITY : (top * p.scale_log2 + log2f(sum)) * 0.69314718055994530942f;
+              p.a.lse[n * p.a.Hq + hd] = log_sum<DT>(top, sum, p.scale_log2);
             }
           };
           // Two ways through the loads: four columns of a row per thread and eight pieces at once, or lane = row, each

@@ -53,3 +53,35 @@ def test_norm_8bit_of_tiny_values(H, group, exponent):
     got = o8.double()
     assert bool((got[y == 0] == 0).all())
     inside(got * big, y, 2.0 ** -4 * y.abs() * (1 + 2.0 ** -14) + 2.0 ** -10 * big + 2.0 ** -16 * y.abs() + 450 * step)
+
+
+# ---- attention ---------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,ctx,new", [(64, 4, 2, [4000, 40], [1, 1]), (128, 8, 1, [40000], [1]),
+                                              (64, 4, 4, [3000, 200], [150, 9]), (128, 24, 2, [6000], [40]),
+                                              (64, 4, 2, [2000] * 160, [1] * 160)])
+@pytest.mark.parametrize("nats", [16.0, 18.0, 20.0])
+def test_attention_f16_small_weights(handle, D, Hq, Hkv, ctx, new, nats):
+    """One key's score lies 16 to 20 above thousands of others' and its value is zero: what is left is
+    the others' sum, though none of their weights is an f16 number of its own beside 1."""
+    c = a_cache(len(ctx) + D, ctx, new, Hq, Hkv, D, 64, F16)
+    c["q"].zero_()
+    c["q"][..., 0] = 8.0
+    c["k"] = torch.where(c["k"].isnan(), c["k"], torch.zeros_like(c["k"]))
+    c["v"] = (100.0 + 10.0 * c["v"].float()).to(F16)
+    for b in range(len(ctx)):
+        first = int(c["table"][b, 0])
+        c["k"][first, 0, :, 0] = nats * D ** 0.5 / 8.0
+        c["v"][first, 0] = 0.0
+    every = 1 if max(new) == 1 else 37
+    want, wl, slack, ls_slack = ref.attention(c["q"], c["k"], c["v"], c["table"], c["q_start"], c["kv_lens"], D ** -0.5,
+                                              every)
+    # a weight is held to half of 2^-24 (f16's smallest) where the largest is at least 2^7: 2^-32 of the
+    # largest, for every key; values are below 160
+    seen = c["kv_lens"].double().max()
+    for hint in (0, max(new)):
+        out, ls = run_attention(handle, c, hint)
+        assert handle.get_error() == 0
+        inside(out, want, ref.stored(want, F16, slack + 160.0 * seen * 2.0 ** -32))
+        inside(ls, wl, ls_slack)
