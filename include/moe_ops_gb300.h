@@ -72,7 +72,9 @@ MOE_API int moe_add_rmsnorm(void* stream, const moe_rmsnorm_args* a);
  * All or nothing: where the free pages, the table's width W or the capacity N do not
  * suffice, or a length is negative, MOE_OPS_ERR_PLAN is raised, the table is left as it
  * is, q_start and kv_lens are zeros, slots are -1, positions 0 and *free_head_out =
- * *free_head. free_head_out must not be free_head (other blocks may still read it).
+ * *free_head. No output (block_table, q_start, kv_lens, positions, slots, free_head_out, err) may
+ * share a word with an input or with another output: other blocks may still read it. Such a call is
+ * refused (MOE_ERR_INVALID_ARG); lengths and the head of the free list are kept in two copies.
  * 1 <= B <= MOE_PLAN_MAX_REQUESTS, page_size a power of two, W * page_size < 2^31. */
 #define MOE_PLAN_MAX_REQUESTS 4096
 typedef struct {

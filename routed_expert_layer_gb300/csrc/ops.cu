@@ -889,6 +889,27 @@ int moe_paged_plan(void* stream, const moe_paged_plan_args* a) {
   for (const void* q : ptrs)
     if (!is_aligned(q, 4)) return MOE_ERR_INVALID_ARG;
   if (a->B > MOE_PLAN_MAX_REQUESTS || (int64_t)a->W * a->page_size >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+  // Every block reads the inputs again after others have begun to write: an output that shares a word with an
+  // input, or with another output, would change positions, slots and table columns, or write past the table.
+  struct {
+    const void* p;
+    int64_t words;
+  } const t[] = {{a->block_table, (a->B - 1) * a->table_stride + a->W},
+                 {a->q_start, (int64_t)a->B + 1},
+                 {a->kv_lens, a->B},
+                 {a->positions, a->N},
+                 {a->slots, a->N},
+                 {a->free_head_out, 1},
+                 {a->err, a->err ? 1 : 0},  // outputs up to here
+                 {a->ctx_lens, a->B},
+                 {a->new_lens, a->B},
+                 {a->free_pages, a->F},
+                 {a->free_head, 1}};
+  for (int o = 0; o < 7; ++o)
+    for (int i = o + 1; i < 11; ++i) {
+      const uintptr_t x = (uintptr_t)t[o].p, y = (uintptr_t)t[i].p;
+      if (x < y + 4 * t[i].words && y < x + 4 * t[o].words && t[o].words && t[i].words) return MOE_ERR_INVALID_ARG;
+    }
   const int blocks = (a->N + kPlanThreads - 1) / kPlanThreads;
   OpsPdl pdl;
   return launch_pdl(plan_kernel, dim3((unsigned)(blocks < 1 ? 1 : blocks > 304 ? 304 : blocks)), dim3(kPlanThreads),

@@ -50,7 +50,8 @@ def paged_plan(ctx_lens, new_lens, block_table, free_pages, free_head, page_size
     """Plan one serving step on the device (moe_paged_plan): from ctx_lens and new_lens [B]
     the new pages (entered into block_table [B][W], taken from free_pages [F] at free_head
     [1]), q_start [B+1], kv_lens [B], positions and slots [N], and the new free_head_out [1].
-    All int32. N may exceed the new tokens: the rest gets position 0 and slot -1."""
+    All int32. N may exceed the new tokens: the rest gets position 0 and slot -1. No output may share
+    memory with an input or another output (kv_lens is not ctx_lens, free_head_out not free_head)."""
     st = _plan(ctx_lens, new_lens, block_table, free_pages, free_head, page_size, q_start, kv_lens, positions, slots,
                free_head_out, err, stream)
     if st:

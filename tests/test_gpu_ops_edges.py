@@ -55,6 +55,43 @@ def test_norm_8bit_of_tiny_values(H, group, exponent):
     inside(got * big, y, 2.0 ** -4 * y.abs() * (1 + 2.0 ** -14) + 2.0 ** -10 * big + 2.0 ** -16 * y.abs() + 450 * step)
 
 
+# ---- plan --------------------------------------------------------------------------------------
+
+
+def test_plan_tensors_of_one_allocation():
+    """Tensors one behind the other in one allocation, the table's rows with other words between them;
+    lengths or the free list's head updated in place are refused."""
+    ctx, new, P, W, stride = [5, 0, 33], [4, 3, 20], 16, 5, 7
+    N, ids = sum(new), [9, 8, 4, 6, 7]
+    sizes = dict(ctx=3, new=3, table=3 * stride, free=5, head=1, q_start=4, kv=3, pos=N, slots=N, head_out=1, err=1)
+    buf = torch.zeros(sum(sizes.values()), dtype=I32, device="cuda")
+    t = dict(zip(sizes, buf.split(list(sizes.values()))))
+    t["table"] = t["table"].view(3, stride)
+    for name, v in (("ctx", ctx), ("new", new), ("free", ids), ("head", [1])):
+        t[name].copy_(ints(v))
+    table = [[3, -1, -1, -1, -1], [-1] * 5, [1, 2, 0, -1, -1]]
+    t["table"].fill_(-7)
+    t["table"][:, :W].copy_(ints(table))
+    before = buf.clone()
+
+    def call(**kw):
+        a = dict(q_start=t["q_start"], kv_lens=t["kv"], positions=t["pos"], slots=t["slots"], free_head_out=t["head_out"], err=t["err"])
+        a.update(kw)
+        rel.paged_plan(t["ctx"], t["new"], t["table"][:, :W], t["free"], t["head"], P, **a)
+
+    for kw in (dict(kv_lens=t["ctx"]), dict(kv_lens=t["new"]), dict(free_head_out=t["head"]), dict(positions=t["slots"]),
+               dict(q_start=buf[1:5]), dict(err=t["head"])):
+        with pytest.raises(rel.MoeError) as e:
+            call(**kw)
+        assert e.value.status == rel.MOE_ERR_INVALID_ARG and torch.equal(buf, before)
+    call()
+    want = ref.plan(ctx, new, table, ids, 1, P, N)
+    for name, key in (("q_start", "q_start"), ("kv", "kv_lens"), ("pos", "positions"), ("slots", "slots"), ("head_out", "free_head_out")):
+        assert t[name].tolist() == want[key], key
+    assert t["table"][:, :W].tolist() == want["block_table"] and bool((t["table"][:, W:] == -7).all())
+    assert t["ctx"].tolist() == ctx and t["new"].tolist() == new and t["free"].tolist() == ids and t["err"].tolist() == [0]
+
+
 # ---- attention ---------------------------------------------------------------------------------
 
 

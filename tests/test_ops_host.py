@@ -103,6 +103,34 @@ def test_plan_refusals(L, kw, status):
     assert L.moe_paged_plan(None, None) == BAD
 
 
+def plan_memory():
+    """Addresses, sizes in words and lengths of a plan call whose tensors lie one behind the other."""
+    B, W, F, N = 4, 8, 10, 6
+    words = dict(ctx_lens=B, new_lens=B, block_table=(B - 1) * 9 + W, free_pages=F, free_head=1, q_start=B + 1, kv_lens=B,
+                 positions=N, slots=N, free_head_out=1, err=1)
+    at, base = {}, 1 << 20
+    for name, n in words.items():
+        at[name] = base
+        base += 4 * n
+    return at, words, dict(table_stride=9, B=B, W=W, F=F, N=N, page_size=16)
+
+
+OUTPUTS = ["block_table", "q_start", "kv_lens", "positions", "slots", "free_head_out", "err"]
+
+
+@pytest.mark.parametrize("out", OUTPUTS)
+def test_plan_refuses_outputs_that_are_inputs_or_each_other(L, out):
+    """No output may share a word with an input (other blocks still read it) or with another output:
+    refused at the tensor's first word and at its last."""
+    at, words, sizes = plan_memory()
+    for other in words:
+        if other == out:
+            continue
+        for place in (at[other], at[other] + 4 * (words[other] - 1), at[other] - 4 * (words[out] - 1)):
+            moved = dict(at, **{out: place})
+            assert L.moe_paged_plan(None, pack("moe_paged_plan_args", **moved, **sizes)) == BAD, (out, other)
+
+
 def rotary_args(**kw):
     base = dict(q=A, k=B_, v=C, q_out=A, k_cache=D_, v_cache=E_, positions=F_, slots=F_, inv_freq=F_, q_tok=512,
                 q_head=128, k_tok=128, k_head=128, v_tok=128, v_head=128, qo_tok=512, qo_head=128, kc_page=2048,
