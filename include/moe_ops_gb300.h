@@ -39,6 +39,8 @@ extern "C" {
  *   over each `group` = 128 consecutive elements (the last block may be shorter); s in
  *   scales[row][block]. A block of zeros has s = 0 and zeros in out8, and so has one whose values are
  *   at most 448 * 2^-150, for which s rounds to 0.
+ * The mean is of fp32 squares: it is that of the formula for |t| of 2^-60 to 2^56 (and below, where eps
+ * is 2^-60 or more); a row whose squares overflow is divided by infinity, as by fp32 arithmetic throughout.
  * x, residual, out, residual_out [T][H] with row strides; weight [H] in dtype, or fp32 with
  * weight_f32 = 1. residual_out may be residual itself (in place) and out may be x itself;
  * no other overlap. out or out8 may be NULL (not both); scales goes with out8.
