@@ -160,11 +160,13 @@ typedef struct {
 typedef struct moe_attn_ctx moe_attn_ctx; /* opaque: device workspace and error word */
 
 /* Create a handle on `device` (sm_103). As with moe_ctx, one host thread and one stream
- * use it at a time. */
+ * use it at a time. It is ready for any stream when the call returns (which waits for the
+ * device's default stream). */
 MOE_API int moe_attn_create(int device, moe_attn_ctx** out);
 MOE_API int moe_attn_forward(moe_attn_ctx* ctx, void* stream, const moe_attn_args* a);
 /* Read and clear the handle's device error word (synchronises the device): MOE_OK or
- * MOE_ERR_DEVICE_FLAG, *bits (may be NULL) the raw word (bit 4: a bounded wait gave up). */
+ * MOE_ERR_DEVICE_FLAG, *bits (may be NULL) the raw word (bit 4: a bounded wait gave up; what a
+ * handle computes after that is not valid until this call has cleared it). */
 MOE_API int moe_attn_get_error(moe_attn_ctx* ctx, uint32_t* bits);
 /* Device bytes of the handle's workspace. */
 MOE_API int64_t moe_attn_device_bytes(const moe_attn_ctx* ctx);

@@ -1074,6 +1074,12 @@ int attn_by_rows(const moe_attn_ctx* ctx, const AttnParams& p, cudaStream_t s) {
   return attn_launch<ChunkCfg<DT, D>>(ctx, p, s);
 }
 
+// Clears the error word and the tickets. cudaMemset does not wait, and streams that do not wait for the default one
+// could use the handle before it ran: so this does.
+bool clear_head(const moe_attn_ctx* c) {
+  return cudaMemset(c->mem, 0, c->head_bytes) == cudaSuccess && cudaStreamSynchronize(cudaStreamLegacy) == cudaSuccess;
+}
+
 int attn_check(const moe_attn_args* a) {
   if (!a || a->N < 0 || a->B < 1 || a->Hq < 1 || a->Hkv < 1 || a->Hq % a->Hkv || a->num_pages < 1 || a->W < 1 ||
       a->max_new < 0 || !is_pow2(a->page_size) || a->table_stride < a->W)
@@ -1140,7 +1146,7 @@ int moe_attn_create(int device, moe_attn_ctx** out) {
   c->err = (uint32_t*)c->mem;
   c->tickets = (int32_t*)((char*)c->mem + 256);
   c->parts = (float*)((char*)c->mem + head);
-  if (cudaMemset(c->mem, 0, head) != cudaSuccess || attn_configure<StreamCfg<0, 64>>() != cudaSuccess ||
+  if (!clear_head(c) || attn_configure<StreamCfg<0, 64>>() != cudaSuccess ||
       attn_configure<StreamCfg<0, 128>>() != cudaSuccess || attn_configure<StreamCfg<1, 64>>() != cudaSuccess ||
       attn_configure<StreamCfg<1, 128>>() != cudaSuccess || attn_configure<ChunkCfg<0, 64>>() != cudaSuccess ||
       attn_configure<ChunkCfg<0, 128>>() != cudaSuccess || attn_configure<ChunkCfg<1, 64>>() != cudaSuccess ||
@@ -1186,7 +1192,7 @@ int moe_attn_get_error(moe_attn_ctx* ctx, uint32_t* bits) {
   if (cudaDeviceSynchronize() != cudaSuccess) return MOE_ERR_CUDA;
   if (cudaMemcpy(&v, ctx->err, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
   // a kernel that gave up leaves its tickets behind
-  if (v && cudaMemset(ctx->mem, 0, ctx->head_bytes) != cudaSuccess) return MOE_ERR_CUDA;
+  if (v && !clear_head(ctx)) return MOE_ERR_CUDA;
   if (bits) *bits = v;
   return v ? MOE_ERR_DEVICE_FLAG : MOE_OK;
 }

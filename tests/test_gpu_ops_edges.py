@@ -122,3 +122,13 @@ def test_attention_f16_small_weights(handle, D, Hq, Hkv, ctx, new, nats):
         assert handle.get_error() == 0
         inside(out, want, ref.stored(want, F16, slack + 160.0 * seen * 2.0 ** -32))
         inside(ls, wl, ls_slack)
+
+
+def test_handle_is_ready_on_every_stream():
+    """A new handle's workspace has been cleared when the call returns, whatever the default stream was
+    busy with: streams that do not wait for that one may use the handle at once."""
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # some 0.1 s of the default stream
+    h = rel.PagedAttention(device=0)
+    assert torch.cuda.default_stream().query()
+    h.close()
