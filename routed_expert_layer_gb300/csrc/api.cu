@@ -69,6 +69,10 @@ struct DeviceGuard {
   }
 };
 
+// cudaMemset, and cudaMemcpy from pageable memory, return before the device is done, and neither the streams that load
+// a layer nor a user's that do not wait for the default stream come behind them: what clears or copies waits here.
+bool default_stream_done() { return cudaStreamSynchronize(cudaStreamLegacy) == cudaSuccess; }
+
 // Programmatic dependent launch for the kernels one forward enqueues (decode sizes).
 struct PdlScope {
   explicit PdlScope(bool on) { g_launch_pdl = on; }
@@ -481,7 +485,7 @@ int moe_create(const moe_config* cfg, int device, moe_ctx** out) {
   workspace_layout(*cfg, ctx->sm_count, &ctx->ws, (char*)ctx->ws_mem);
   const uint64_t rows = (uint64_t)cfg->max_tokens * cfg->top_k;
   if (cudaMemset(ctx->ws.err, 0, sizeof(uint32_t)) != cudaSuccess ||
-      cudaMemset(ctx->ws.ticket, 0, sizeof(uint32_t)) != cudaSuccess ||
+      cudaMemset(ctx->ws.ticket, 0, sizeof(uint32_t)) != cudaSuccess || !default_stream_done() ||
       !make_tmap_16(&ctx->tmap_x, ctx->ws.xg, rows, ctx->sh.D, 16, false) ||
       !make_tmap_16(&ctx->tmap_h, ctx->ws.h16, rows, cfg->inter, 16, false) ||
       !make_tmap_16(&ctx->tmap_x64, ctx->ws.xg, rows, ctx->sh.D, 64, false) ||
@@ -549,7 +553,7 @@ int moe_load_layer(moe_ctx* ctx, const moe_layer_host* lh) {
              : cudaMemset(W.router_bias, 0, E * sizeof(float))) != cudaSuccess ||
         cudaMemcpy(W.gu_global, lh->gu_global, 2 * El * sizeof(float), cudaMemcpyHostToDevice) != cudaSuccess ||
         cudaMemcpy(W.dn_global, lh->dn_global, El * sizeof(float), cudaMemcpyHostToDevice) != cudaSuccess ||
-        cudaMemset(W.scale_max, 0, 3 * El * sizeof(uint32_t)) != cudaSuccess) {
+        cudaMemset(W.scale_max, 0, 3 * El * sizeof(uint32_t)) != cudaSuccess || !default_stream_done()) {
       st = MOE_ERR_CUDA;
       break;
     }
@@ -598,7 +602,7 @@ int moe_load_layer(moe_ctx* ctx, const moe_layer_host* lh) {
     }
     if (st == MOE_OK && launch_norms(ctx->sh, W.scale_max, W.gu_norm, W.dn_norm, W.norm_exp, s) != cudaSuccess)
       st = MOE_ERR_CUDA;
-    if (st == MOE_OK && cudaStreamSynchronize(s) != cudaSuccess) st = MOE_ERR_CUDA;
+    if (st == MOE_OK && (cudaStreamSynchronize(s) != cudaSuccess || !default_stream_done())) st = MOE_ERR_CUDA;
   } while (0);
   cudaStreamDestroy(s);
   cudaFree(staging);
@@ -677,7 +681,7 @@ int moe_get_error(moe_ctx* ctx, uint32_t* bits) {
   uint32_t v = 0;
   if (cudaDeviceSynchronize() != cudaSuccess) return MOE_ERR_CUDA;
   if (cudaMemcpy(&v, ctx->ws.err, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
-  if (cudaMemset(ctx->ws.err, 0, sizeof(v)) != cudaSuccess) return MOE_ERR_CUDA;
+  if (cudaMemset(ctx->ws.err, 0, sizeof(v)) != cudaSuccess || !default_stream_done()) return MOE_ERR_CUDA;
   if (bits) *bits = v;
   return v ? MOE_ERR_DEVICE_FLAG : MOE_OK;
 }

@@ -338,3 +338,16 @@ def test_out_of_range_intermediate_raises_the_error_word():
         assert m.get_error() == 0  # read and cleared
     finally:
         m.close()
+
+
+def test_context_is_ready_on_every_stream():
+    """A new context's error word and ticket have been cleared when the call returns, whatever the
+    default stream was busy with: streams that do not wait for that one may use it at once."""
+    import routed_expert_layer_gb300 as rel
+    import torch
+    rel.MoeLayer(256, 128, 32, 4, 16).close()  # (the first one loads the kernels, which waits too)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # some 0.1 s of the default stream
+    moe = rel.MoeLayer(256, 128, 32, 4, 16)
+    assert torch.cuda.default_stream().query()
+    moe.close()
