@@ -142,7 +142,7 @@ int norm(PyObject* const* a) {
   p.group = int32(a[8], "group");
   if (a[6] != Py_None) {
     const at::Tensor& t = tensor(a[6], "out8");
-    if (t.element_size() != 1)
+    if (t.scalar_type() != at::kFloat8_e4m3fn && t.scalar_type() != at::kByte)
       fail(PyExc_ValueError, std::string("out8: expected float8_e4m3fn or uint8, got ") + at::toString(t.scalar_type()));
     p.out8_stride = rows(t, "out8", dims, t.scalar_type(), dev);
     p.out8 = static_cast<uint8_t*>(ptr(t));

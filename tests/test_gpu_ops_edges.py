@@ -55,6 +55,15 @@ def test_norm_8bit_of_tiny_values(H, group, exponent):
     inside(got * big, y, 2.0 ** -4 * y.abs() * (1 + 2.0 ** -14) + 2.0 ** -10 * big + 2.0 ** -16 * y.abs() + 450 * step)
 
 
+@pytest.mark.parametrize("dtype", [torch.float8_e5m2, torch.int8, torch.bool])
+def test_norm_8bit_types(dtype):
+    """Bits of e4m3 go to tensors of that type or of bytes only."""
+    x, w = randn(gen(1), 3, 256), randn(gen(2), 256)
+    o8, sc = torch.empty(3, 256, dtype=dtype, device="cuda"), torch.empty(3, 1, device="cuda")
+    with pytest.raises(ValueError, match="float8_e4m3fn or uint8"):
+        rel.add_rmsnorm(x, w, 1e-6, out8=o8, scales=sc)
+
+
 # ---- plan --------------------------------------------------------------------------------------
 
 
