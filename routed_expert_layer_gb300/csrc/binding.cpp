@@ -151,6 +151,8 @@ int norm(PyObject* const* a) {
     expect(s, "scales", {T, p.group > 0 ? (H + p.group - 1) / p.group : 1}, at::kFloat, dev);
     if (!s.is_contiguous()) fail(PyExc_ValueError, "scales: expected a contiguous tensor");
     p.scales = static_cast<float*>(ptr(s));
+  } else if (a[7] != Py_None) {
+    fail(PyExc_ValueError, "scales: only with out8");
   }
   p.err = err_word(a[9], dev);
   p.T = int32(T, "x");

@@ -64,6 +64,12 @@ def test_norm_8bit_types(dtype):
         rel.add_rmsnorm(x, w, 1e-6, out8=o8, scales=sc)
 
 
+def test_norm_scales_need_8bit_output():
+    x, w = randn(gen(1), 3, 256), randn(gen(2), 256)
+    with pytest.raises(ValueError, match="scales"):
+        rel.add_rmsnorm(x, w, 1e-6, out=torch.empty_like(x), scales=torch.empty(3, 1, device="cuda"))
+
+
 # ---- plan --------------------------------------------------------------------------------------
 
 
