@@ -77,7 +77,8 @@ MOE_API int moe_add_rmsnorm(void* stream, const moe_rmsnorm_args* a);
  * *free_head. No output (block_table, q_start, kv_lens, positions, slots, free_head_out, err) may
  * share a word with an input or with another output: other blocks may still read it. Such a call is
  * refused (MOE_ERR_INVALID_ARG); lengths and the head of the free list are kept in two copies.
- * 1 <= B <= MOE_PLAN_MAX_REQUESTS, page_size a power of two, W * page_size < 2^31. */
+ * 1 <= B <= MOE_PLAN_MAX_REQUESTS, F >= 0 (0: free_pages may be NULL), N >= 0 (0: positions and
+ * slots may be NULL), page_size a power of two, W * page_size < 2^31. */
 #define MOE_PLAN_MAX_REQUESTS 4096
 typedef struct {
   const int32_t* ctx_lens;

@@ -878,8 +878,8 @@ int moe_add_rmsnorm(void* stream, const moe_rmsnorm_args* a) {
 }
 
 int moe_paged_plan(void* stream, const moe_paged_plan_args* a) {
-  if (!a || !a->ctx_lens || !a->new_lens || !a->block_table || !a->free_pages || !a->free_head || !a->q_start ||
-      !a->kv_lens || !a->free_head_out || a->free_head == a->free_head_out)
+  if (!a || !a->ctx_lens || !a->new_lens || !a->block_table || !a->free_head || !a->q_start || !a->kv_lens ||
+      !a->free_head_out || (a->F > 0 && !a->free_pages))
     return MOE_ERR_INVALID_ARG;
   if (a->B < 1 || a->W < 1 || a->F < 0 || a->N < 0 || a->table_stride < a->W || !is_pow2(a->page_size))
     return MOE_ERR_INVALID_ARG;

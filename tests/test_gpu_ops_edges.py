@@ -107,6 +107,23 @@ def test_plan_tensors_of_one_allocation():
     assert t["ctx"].tolist() == ctx and t["new"].tolist() == new and t["free"].tolist() == ids and t["err"].tolist() == [0]
 
 
+def test_plan_without_free_pages():
+    """A step inside the pages its requests have needs no free page; one that needs a page is refused whole."""
+    empty, err = torch.empty(0, dtype=I32, device="cuda"), ints([0])
+    for new, fits in (([1, 2], True), ([1, 20], False)):
+        table = ints([[3, -1], [5, 1]])
+        q_start, kv, pos, slots, head = (ints([9] * n) for n in (3, 2, sum(new), sum(new), 1))
+        err.zero_()
+        rel.paged_plan(ints([2, 17]), ints(new), table, empty, ints([0]), 16, q_start=q_start, kv_lens=kv, positions=pos,
+                       slots=slots, free_head_out=head, err=err)
+        assert table.tolist() == [[3, -1], [5, 1]] and head.tolist() == [0]
+        if fits:
+            assert err.tolist() == [0] and q_start.tolist() == [0, 1, 3] and kv.tolist() == [3, 19]
+            assert pos.tolist() == [2, 17, 18] and slots.tolist() == [50, 17, 18]
+        else:
+            assert err.tolist() == [rel.MOE_OPS_ERR_PLAN] and kv.tolist() == [0, 0] and set(slots.tolist()) == {-1}
+
+
 # ---- attention ---------------------------------------------------------------------------------
 
 
