@@ -134,7 +134,8 @@ MOE_API int moe_rotary_append(void* stream, const moe_rotary_args* a);
  *   lse[n][h] = ln sum_j exp(scale * q . k_j)   (fp32 [N][Hq], or NULL)
  * A row that sees no key (kv_lens < new) gets zeros and lse = -inf. Keys a row does not
  * see never reach it, whatever they hold. fp32 scores and sums; the weights are rounded to
- * dtype for the second product. Rows of q outside every request are not written.
+ * dtype for the second product. Rows of q outside every request are not written; without rows
+ * or without requests (N or B = 0) nothing is.
  * A page outside [0, num_pages) raises MOE_OPS_ERR_INDEX and counts as zeros; kv_lens beyond the
  * table's W * P raises it and counts as W * P (below 0: as 0); a request whose rows lie outside
  * [0, N] raises it and is skipped.

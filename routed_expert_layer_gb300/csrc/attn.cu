@@ -1081,7 +1081,7 @@ bool clear_head(const moe_attn_ctx* c) {
 }
 
 int attn_check(const moe_attn_args* a) {
-  if (!a || a->N < 0 || a->B < 1 || a->Hq < 1 || a->Hkv < 1 || a->Hq % a->Hkv || a->num_pages < 1 || a->W < 1 ||
+  if (!a || a->N < 0 || a->B < 0 || a->Hq < 1 || a->Hkv < 1 || a->Hq % a->Hkv || a->num_pages < 1 || a->W < 1 ||
       a->max_new < 0 || !is_pow2(a->page_size) || a->table_stride < a->W)
     return MOE_ERR_INVALID_ARG;
   if (a->dtype != MOE_DT_BF16 && a->dtype != MOE_DT_F16) return MOE_ERR_INVALID_ARG;
@@ -1089,7 +1089,7 @@ int attn_check(const moe_attn_args* a) {
   if ((a->D != 64 && a->D != 128) || a->Hq / a->Hkv > 128 || a->page_size < 16 || a->page_size > 1024 ||
       (int64_t)a->W * a->page_size >= ((int64_t)1 << 30) || (int64_t)a->N * a->Hq >= ((int64_t)1 << 31))
     return MOE_ERR_UNSUPPORTED;
-  if (a->N == 0) return MOE_OK;
+  if (a->N == 0 || a->B == 0) return MOE_OK;
   const void* t16[] = {a->q, a->k_cache, a->v_cache, a->out};
   for (const void* p : t16)
     if (!p || !is_aligned(p, 16)) return MOE_ERR_INVALID_ARG;
@@ -1163,7 +1163,7 @@ int moe_attn_create(int device, moe_attn_ctx** out) {
 int moe_attn_forward(moe_attn_ctx* ctx, void* stream, const moe_attn_args* a) {
   if (!ctx) return MOE_ERR_INVALID_ARG;
   const int st = attn_check(a);
-  if (st != MOE_OK || a->N == 0) return st;
+  if (st != MOE_OK || a->N == 0 || a->B == 0) return st;
   DeviceGuard g(ctx->device);
   AttnParams p;
   p.a = *a;

@@ -164,3 +164,13 @@ def test_handle_is_ready_on_every_stream():
     h = rel.PagedAttention(device=0)
     assert torch.cuda.default_stream().query()
     h.close()
+
+
+def test_attention_without_requests(handle):
+    """A call without requests, with rows of q or without, writes nothing."""
+    c = a_cache(14, [10], [2], 4, 2, 64, 16, BF16)
+    none = torch.empty(0, dtype=I32, device="cuda")
+    for rows in (0, 2):
+        out = torch.full_like(c["q"][:rows], 3.0)
+        handle.forward(c["q"][:rows], c["k"], c["v"], c["table"][:0], ints([0]), none, out, scale=1.0)
+        assert bool((out == 3.0).all()) and handle.get_error() == 0
