@@ -141,7 +141,7 @@ MOE_API int moe_rotary_append(void* stream, const moe_rotary_args* a);
  * [0, N] raises it and is skipped.
  * D is 64 or 128, Hq % Hkv == 0, Hq / Hkv <= 128, P a power of two of 16 to 1024, W * P < 2^30,
  * pointers 16-byte aligned and strides multiples of 8 elements (lse, tables: 4 bytes),
- * scale > 0, out must not overlap q. max_new: the most new tokens a request of this call
+ * scale > 0, out shares no element with q. max_new: the most new tokens a request of this call
  * has, if known, else 0; it chooses a variant and never changes what is computed. */
 typedef struct {
   const void* q;

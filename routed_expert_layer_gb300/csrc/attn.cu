@@ -49,6 +49,7 @@
 // faster; a second S tile per row tile with one row tile per CTA 440 us against 326 for decoding; output rows
 // staged through shared memory 1.99 ms.
 #include <algorithm>
+#include <cstdlib>
 #include <numeric>
 
 #include "ops_internal.cuh"
@@ -1080,6 +1081,23 @@ bool clear_head(const moe_attn_ctx* c) {
   return cudaMemset(c->mem, 0, c->head_bytes) == cudaSuccess && cudaStreamSynchronize(cudaStreamLegacy) == cudaSuccess;
 }
 
+// Whether q and out share an element. Tensors of the same strides whose spans meet may still lie beside each other (as
+// halves of a row or of a head, or in every other row): then element (n, h, d) of out is one of q's where their distance
+// is dn tokens, dh heads and dd elements, each less than the tensor has.
+bool shares_elements(const moe_attn_args* a) {
+  if (!overlap(span16(a->q, a->N, a->q_tok, a->Hq, a->q_head, a->D), span16(a->out, a->N, a->out_tok, a->Hq, a->out_head, a->D)))
+    return false;
+  if ((a->N > 1 && a->q_tok != a->out_tok) || (a->Hq > 1 && a->q_head != a->out_head)) return true;
+  const int64_t apart = ((const char*)a->out - (const char*)a->q) / 2;
+  for (int64_t dh = 1 - a->Hq; dh < a->Hq; ++dh) {
+    const int64_t rest = apart - (a->Hq > 1 ? dh * a->q_head : 0);
+    const int64_t most = a->N - 1, near = most ? std::max(-most, std::min(most, rest / a->q_tok)) : 0;
+    for (int64_t dn = near - 1; dn <= near + 1; ++dn)
+      if (std::abs(dn) <= most && std::abs(rest - (most ? dn * a->q_tok : 0)) < a->D) return true;
+  }
+  return false;
+}
+
 int attn_check(const moe_attn_args* a) {
   if (!a || a->N < 0 || a->B < 0 || a->Hq < 1 || a->Hkv < 1 || a->Hq % a->Hkv || a->num_pages < 1 || a->W < 1 ||
       a->max_new < 0 || !is_pow2(a->page_size) || a->table_stride < a->W)
@@ -1106,9 +1124,7 @@ int attn_check(const moe_attn_args* a) {
   for (const void* p : t32)
     if (!p || !is_aligned(p, 4)) return MOE_ERR_INVALID_ARG;
   if (!is_aligned(a->lse, 4)) return MOE_ERR_INVALID_ARG;
-  if (overlap(span16(a->q, a->N, a->q_tok, a->Hq, a->q_head, a->D),
-              span16(a->out, a->N, a->out_tok, a->Hq, a->out_head, a->D)))
-    return MOE_ERR_INVALID_ARG;
+  if (shares_elements(a)) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 

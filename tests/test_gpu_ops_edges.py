@@ -174,3 +174,29 @@ def test_attention_without_requests(handle):
         out = torch.full_like(c["q"][:rows], 3.0)
         handle.forward(c["q"][:rows], c["k"], c["v"], c["table"][:0], ints([0]), none, out, scale=1.0)
         assert bool((out == 3.0).all()) and handle.get_error() == 0
+
+
+@pytest.mark.parametrize("by", ["columns", "heads", "rows"])
+def test_attention_out_beside_q(handle, by):
+    """q and out in one allocation without a shared element: halves of a row, of a head's row, every
+    other row."""
+    c = a_cache(15, [30, 70], [20, 3], 6, 2, 64, 16, BF16)
+    want, _ = run_attention(handle, c)
+    N = c["q"].shape[0]
+    if by == "columns":
+        buf = torch.zeros(N, 12, 64, dtype=BF16, device="cuda")
+        q, out = buf[:, 6:], buf[:, :6]
+    elif by == "heads":
+        buf = torch.zeros(N, 6, 128, dtype=BF16, device="cuda")
+        q, out = buf[..., :64], buf[..., 64:]
+    else:
+        buf = torch.zeros(2 * N, 6, 64, dtype=BF16, device="cuda")
+        q, out = buf[1::2], buf[::2]
+    q.copy_(c["q"])
+    run_attention(handle, dict(c, q=q), out=out)
+    assert torch.equal(out, want) and torch.equal(q, c["q"])
+    with pytest.raises(rel.MoeError):
+        run_attention(handle, dict(c, q=q), out=q)
+    if by == "columns":
+        with pytest.raises(rel.MoeError):  # the last head of one is the first of the other
+            run_attention(handle, dict(c, q=buf[:, 5:11]), out=buf[:, :6])
