@@ -54,7 +54,9 @@ class DecoderLayer:
 
     def step(self, x, residual, new: list[int]):
         """x, residual [sum(new)][H]: the layer below's output and the residual stream of each
-        request's new tokens, request after request. Returns (expert output, residual, norm2 output)."""
+        request's new tokens, request after request. Returns (expert output, residual, norm2 output).
+        A step that does not fit the cache raises MOE_OPS_ERR_PLAN in self.err and leaves the layer's
+        state as it was; what it returns is of no use."""
         N, B = sum(new), len(new)
         i32 = dict(dtype=torch.int32, device=x.device)
         new_lens = torch.tensor(new, **i32)
@@ -69,14 +71,15 @@ class DecoderLayer:
         a, b = self.Hq * self.D, (self.Hq + self.Hkv) * self.D
         q, k, v = (t.view(N, -1, self.D) for t in (qkv[:, :a], qkv[:, a:b], qkv[:, b:]))
         rel.rotary_append(q, k, v, positions, slots, self.inv_freq, self.k_cache, self.v_cache, err=self.err)  # q in place
-        o = torch.empty(N, self.Hq, self.D, dtype=x.dtype, device=x.device)
+        # zeros: where the plan refuses the step (self.err says so) there is no request whose rows attention writes
+        o = torch.zeros(N, self.Hq, self.D, dtype=x.dtype, device=x.device)
         self.attention.forward(q, self.k_cache, self.v_cache, self.table, q_start, kv_lens, o, scale=self.D ** -0.5,
                                max_new=max(new))
         m = torch.empty_like(x)
         rel.add_rmsnorm(o.view(N, a) @ self.w_o, self.norm2, 1e-6, out=m, residual=h, residual_out=h)
         out = torch.empty_like(x)
         self.moe.forward(m, out)
-        self.ctx = kv_lens
+        self.ctx = self.ctx + q_start.diff()  # what the step brought: nothing if it was refused, where kv_lens is zeros
         self.heads = self.heads.flip(0)
         return out, h, m
 

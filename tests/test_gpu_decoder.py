@@ -77,3 +77,37 @@ def test_example_runs(capsys):
     import decoder_layer
     decoder_layer.main()
     assert "max difference" in capsys.readouterr().out
+
+
+def test_refused_step_leaves_the_layer_as_it_was():
+    """A step past the cache is reported, and the steps after it go on from the lengths and pages before it."""
+    from decoder_layer import DecoderLayer
+    H, I, E, k = 512, 256, 64, 8
+    moe = rel.MoeLayer(H, I, E, k, max_tokens=512)
+    moe.load(synth.layer(H, I, E, seed_weights=1, seed_router=2))
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    x, residual = ([torch.randn(n, H, generator=g, device="cuda").bfloat16() for n in (25, 15)] for _ in range(2))
+
+    def step(layer, a, b):
+        rows = [slice(*a), slice(*b)]
+        return layer.step(torch.cat([t[r] for t, r in zip(x, rows)]), torch.cat([t[r] for t, r in zip(residual, rows)]),
+                          [a[1] - a[0], b[1] - b[0]])
+
+    results = []
+    for refused in (False, True):
+        layer = DecoderLayer(moe, q_heads=8, kv_heads=2, head_dim=64, requests=2, max_len=32, page_size=16)
+        step(layer, (0, 20), (0, 10))
+        if refused:
+            kept = layer.table.clone()
+            step(layer, (0, 13), (10, 11))  # 33 tokens of 32
+            assert int(layer.err.item()) == rel.MOE_OPS_ERR_PLAN
+            layer.err.zero_()
+            assert layer.ctx.tolist() == [20, 10] and int(layer.heads[0].item()) == 3 and torch.equal(layer.table, kept)
+        results.append(step(layer, (20, 25), (10, 15)))
+        torch.cuda.synchronize()
+        assert layer.ctx.tolist() == [25, 15] and int(layer.err.item()) == 0
+        assert layer.attention.get_error() == 0 and moe.get_error() == 0
+        layer.close()
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    moe.close()
