@@ -104,7 +104,8 @@ def run(layer, x, residual, lengths, steps):
     return back
 
 
-def main() -> None:
+def main() -> list:
+    """Returns each request's residual stream whole and in steps."""
     import synth
     H, I, E, k = 512, 256, 64, 8
     lengths = [333, 70, 1]
@@ -122,10 +123,12 @@ def main() -> None:
         torch.cuda.synchronize()
         assert int(layer.err.item()) == 0 and layer.attention.get_error() == 0 and moe.get_error() == 0
         layer.close()
-    off = max(float((a.float() - b.float()).abs().max()) for a, b in zip(results[0][1], results[1][1]))
+    pairs = list(zip(results[0][1], results[1][1]))
+    off = max(float((a.float() - b.float()).abs().max()) for a, b in pairs)
     print(f"{sum(lengths)} tokens of {len(lengths)} requests: residual stream whole against in {len(chunks)} steps, "
           f"max difference {off:.3g}")
     moe.close()
+    return pairs
 
 
 if __name__ == "__main__":

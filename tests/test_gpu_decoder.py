@@ -111,3 +111,13 @@ def test_refused_step_leaves_the_layer_as_it_was():
         layer.close()
     assert all(torch.equal(a, b) for a, b in zip(*results))
     moe.close()
+
+
+def test_example_agrees_with_itself():
+    """The example's residual streams, fed whole and in steps, differ by no more than each may from the
+    64-bit layer's: 2^-6 of the larger of the value and 2 (test_decoder_layer_in_steps), so twice that."""
+    import decoder_layer
+    for whole, steps in decoder_layer.main():
+        a, b = whole.double(), steps.double()
+        assert whole.shape == steps.shape and bool(a.isfinite().all())
+        assert float(((a - b).abs() / a.abs().clamp(min=2.0)).max()) <= 2.0 ** -5 * (1 + 2.0 ** -5)
