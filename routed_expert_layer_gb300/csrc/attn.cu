@@ -138,7 +138,7 @@ __device__ __forceinline__ int64_t div_floor(int64_t a, int64_t b) {
 
 // The axis and the calling CTA's stretch [x0, x1) of it: CTA c of n starts at c * (total / n) + min(c, total % n).
 struct Axis {
-  int64_t total, each, x0, x1, whole;
+  int64_t each, x0, x1, whole;
   int n, extra;
   __device__ __forceinline__ int64_t start(int c) const { return c * each + min(c, extra); }
   __device__ __forceinline__ int owner(int64_t x) const {  // the CTA whose stretch holds x
@@ -406,7 +406,6 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
   }
   __syncthreads();
   Axis ax;
-  ax.total = total;
   ax.n = (int)max((int64_t)1, min((int64_t)gridDim.x, total / kMinStretch<QT>));
   ax.each = div_floor(total, ax.n);
   ax.extra = (int)(total - ax.each * ax.n);

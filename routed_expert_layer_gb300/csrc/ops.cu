@@ -525,8 +525,9 @@ cudaError_t norm_any_by_size(const NormParams& p, cudaStream_t s) {
   if (n <= 2048) return launch_norm_any<DT, VE, 256, 8, 5>(p, s);
   if (n <= 4096) return launch_norm_any<DT, VE, 256, 16, 4>(p, s);
   if (n <= 8192) return launch_norm_any<DT, VE, 512, 16, 2>(p, s);
-  if (VE == 2 || n <= 16384) return launch_norm_any<DT, VE, 1024, 16, 1>(p, s);
-  return launch_norm_any<DT, VE, 1024, VE == 2 ? 16 : 32, 1>(p, s);
+  if constexpr (VE == 1)
+    if (n > 16384) return launch_norm_any<DT, VE, 1024, 32, 1>(p, s);
+  return launch_norm_any<DT, VE, 1024, 16, 1>(p, s);
 }
 
 template <int DT>

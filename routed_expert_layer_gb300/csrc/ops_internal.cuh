@@ -39,17 +39,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Reads a kernel's parameters before it waits for the kernel before it, so that their first use after the
-// wait does not miss the constant cache; the sum goes to a word of shared memory nobody has used yet.
-template <class P>
-__device__ __forceinline__ void touch_params(const P& p, volatile uint32_t* unused) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(&p);
-  uint32_t sum = 0;
-#pragma unroll
-  for (int i = 0; i < (int)(sizeof(P) / 4); i += 8) sum ^= w[i];
-  *unused = sum;
-}
-
 inline bool is_aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 inline bool is_pow2(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
 
