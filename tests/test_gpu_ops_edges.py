@@ -200,3 +200,96 @@ def test_attention_out_beside_q(handle, by):
     if by == "columns":
         with pytest.raises(rel.MoeError):  # the last head of one is the first of the other
             run_attention(handle, dict(c, q=buf[:, 5:11]), out=buf[:, :6])
+
+
+@pytest.mark.parametrize("B", [128, 129, 257, 600])
+@pytest.mark.parametrize("top", [1, 40])
+def test_attention_many_requests(handle, B, top):
+    """More requests than a CTA keeps cost sums for, idle ones at both ends of the batch, at the ends of
+    the runs that share a sum, and whole runs of them."""
+    r = random.Random(B + top)
+    seg = -(-B // 128)
+    ctx, new = [], []
+    for b in range(B):
+        idle = b < 5 or b >= B - 4 or b % (3 * seg) >= 2 * seg or b % seg == seg - 1 and r.random() < 0.5
+        ctx.append(r.choice([0, 1, 63, 64, r.randint(0, 200), r.randint(0, 900) if b % 50 == 9 else 5]))
+        new.append(0 if idle else r.choice([1, 1, 1, r.randint(1, top)]))
+    c = a_cache(B + top, ctx, new, 4, 2, 64, 16, BF16)
+    check_attention(handle, c)
+    check_attention(handle, c, max_new=top)
+    check_attention(handle, c, max_new=1)
+
+
+# ---- streams and graphs ------------------------------------------------------------------------
+
+
+def test_two_handles_on_two_streams(handle):
+    """Two handles at work at once, each on a stream of its own, give what each gives alone."""
+    other = rel.PagedAttention(device=0)
+    calls = [a_cache(21, [5000, 10, 700], [1, 200, 3], 24, 2, 128, 64, BF16), a_cache(22, [9000, 40], [1, 2], 24, 2, 128, 64, BF16)]
+    want = [run_attention(handle, c)[0].clone() for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    outs = [torch.empty_like(w) for w in want]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for h, c, out, s in zip((handle, other), calls, outs, streams):
+            h.forward(c["q"], c["k"], c["v"], c["table"], c["q_start"], c["kv_lens"], out, scale=128 ** -0.5, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    assert handle.get_error() == 0 and other.get_error() == 0
+    other.close()
+
+
+def test_step_on_another_stream_and_in_a_graph():
+    """Plan, rotary with its append and the norm, one behind the other on a side stream and from a
+    CUDA graph of all three, give what they give call by call."""
+    g = gen(31)
+    B, P, Hq, Hkv, D = 70, 16, 6, 2, 64
+    r = random.Random(31)
+    ctx, new = [r.randint(0, 90) for _ in range(B)], [r.choice([0, 1, 9]) for _ in range(B)]
+    N, W = sum(new), 8
+    ids = list(range(B * W))
+    r.shuffle(ids)
+    table0 = ints([[ids.pop() for _ in range(-(-t // P))] + [-1] * (W - -(-t // P)) for t in ctx])
+    lens, fresh, free = ints(ctx), ints(new), ints(ids)
+    q, k, v = (randn(g, N, h, D) for h in (Hq, Hkv, Hkv))
+    x, res, w = randn(g, N, 2048), randn(g, N, 2048), randn(g, 2048)
+    f = rel.rope_frequencies(D)
+
+    def buffers():
+        return dict(table=table0.clone(), q_start=ints([0] * (B + 1)), kv=ints([0] * B), pos=ints([0] * N), slots=ints([0] * N),
+                    head=ints([0]), q=torch.empty_like(q), kc=torch.zeros(B * W, P, Hkv, D, dtype=BF16, device="cuda"),
+                    vc=torch.zeros(B * W, P, Hkv, D, dtype=BF16, device="cuda"), h=torch.empty_like(x), n=torch.empty_like(x),
+                    n8=torch.empty(N, 2048, dtype=torch.uint8, device="cuda"), sc=torch.empty(N, 16, device="cuda"))
+
+    head = ints([3])
+
+    def step(b, stream=None):
+        rel.paged_plan(lens, fresh, b["table"], free, head, P, q_start=b["q_start"], kv_lens=b["kv"], positions=b["pos"],
+                       slots=b["slots"], free_head_out=b["head"], stream=stream)
+        rel.rotary_append(q, k, v, b["pos"], b["slots"], f, b["kc"], b["vc"], q_out=b["q"], stream=stream)
+        rel.add_rmsnorm(x, w, 1e-6, out=b["n"], residual=res, residual_out=b["h"], out8=b["n8"], scales=b["sc"], group=128,
+                        stream=stream)
+
+    want, side, captured = buffers(), buffers(), buffers()
+    rel.paged_plan(lens, fresh, want["table"], free, head, P, q_start=want["q_start"], kv_lens=want["kv"],
+                   positions=want["pos"], slots=want["slots"], free_head_out=want["head"])
+    torch.cuda.synchronize()
+    plan = ref.plan(ctx, new, table0.tolist(), ids, 3, P, N)
+    assert want["slots"].tolist() == plan["slots"] and want["table"].tolist() == plan["block_table"]
+    want["table"].copy_(table0)
+    step(want)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    step(side, s)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step(captured)
+    for _ in range(2):
+        captured["table"].copy_(table0)
+        captured["kc"].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+    for name in want:
+        assert torch.equal(want[name], side[name]) and torch.equal(want[name], captured[name]), name
