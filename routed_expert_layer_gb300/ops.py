@@ -68,9 +68,13 @@ def rope_frequencies(rot: int, base: float = 10000.0, linear: float = 1.0, blend
     0.1 ln(factor) + 1, is rotary_append's mscale.)"""
     if rot < 2 or rot % 2:
         raise ValueError("rope_frequencies: rot must be even and positive")
+    if not (base > 0.0 and linear > 0.0):
+        raise ValueError("rope_frequencies: base and linear must be positive")
     f = base ** (-2.0 * torch.arange(rot // 2, dtype=torch.float64) / rot) / linear
     if blend is not None:
         factor, trained, slow, fast = blend
+        if not (factor > 0.0 and trained > 0.0 and slow < fast):
+            raise ValueError("rope_frequencies: blend is (factor, trained, slow, fast), positive and slow below fast")
         keep = ((trained * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0.0, 1.0)
         f = f * (keep + (1.0 - keep) / factor)
     return f.to(device)

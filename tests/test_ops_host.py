@@ -198,6 +198,15 @@ def test_rope_frequencies():
             rel.rope_frequencies(bad, device="cpu")
 
 
+@pytest.mark.parametrize("kw", [dict(base=0.0), dict(base=-2.0), dict(linear=0.0), dict(linear=math.nan),
+                                dict(blend=(8.0, 2048.0, 32.0, 1.0)), dict(blend=(8.0, 2048.0, 1.0, 1.0)),
+                                dict(blend=(0.0, 2048.0, 1.0, 32.0)), dict(blend=(8.0, -1.0, 1.0, 32.0))])
+def test_rope_frequencies_refusals(kw):
+    """Turns given fast before slow would keep the slow pairs and slow the fast ones."""
+    with pytest.raises(ValueError):
+        rel.rope_frequencies(64, device="cpu", **kw)
+
+
 def test_package_knows_its_operators():
     with pytest.raises(AttributeError):
         rel.no_such_operator
