@@ -106,7 +106,8 @@ MOE_API int moe_paged_plan(void* stream, const moe_paged_plan_args* a);
  * Token n's k and v heads go to the cache at page slots[n] / P, row slots[n] % P; slot -1
  * skips the append (q is still rotated); a slot outside [-1, num_pages * P) raises
  * MOE_OPS_ERR_INDEX and is skipped. Two tokens must not share a slot.
- * q, q_out [N][Hq][D], k, v [N][Hkv][D] with token and head strides (q_out may be q);
+ * q, q_out [N][Hq][D], k, v [N][Hkv][D] with token and head strides (q_out may be q, with its
+ * strides; no other output shares an element with an input or another output);
  * caches with page, row and head strides (either order of rows and heads).
  * 2 <= rot <= D, rot even, D even, D <= 1024, P a power of two, num_pages * P < 2^31. */
 typedef struct {

@@ -107,17 +107,20 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
 // norm_staged_kernel (1024 < H <= 14336, 16-byte chunks): blocks stay and walk over the rows, the next
 // rows' bytes come by bulk copies into two stages of shared memory, so the reduction's latency is
 // not added to memory's, and the weights are loaded once per block. At T = 8192, H = 7168, bf16 with
-// residual and 8-bit blocks: 86 us, 6.1 TB/s. Measured on the way: one row per block and register
+// residual and 8-bit blocks: 87 us, 6.1 TB/s. Measured on the way: one row per block and register
 // loads with 1, 2, 4, 8 chunks per thread 125, 114, 105, 117 us; walking with the next row's loads in
 // registers 95 us; two blocks per SM with 2, 3, 4 stages 86.1, 87.1, 87.5 us, one block with six 111 us,
-// three blocks of 224 threads 97 us. Single rows too: T = 1 2.4 us a launch in a graph (register loads 2.9).
+// three blocks of 224 threads 97 us. Single rows too: T = 1 2.4 us a launch in a graph (register loads 2.9). The limit is
+// 896 threads of two pieces; T = 4096, H = 14336 without, with a row's and with blocks' 8-bit outputs: 81, 85, 82 us,
+// norm_any_kernel in pairs 78, 99, 112. 1,024 threads would reach 16384, and are not built.
 // norm_rows_kernel (H <= 1024, 16-byte chunks): several rows per block, one chunk per thread, the next
 // rows' loads issued before this one's reduction; staging rows this short would cost a copy each. Both at
-// T = 8192: H = 128 4.5 us (staged 6.3), 512 7.6 (8.4), 1024 13.1 (13.1); T = 1, H = 512 1.8 us (2.6).
+// T = 8192: H = 128 4.6 us (staged 6.3), 512 7.7 (8.4), 1024 13.4 (13.1); T = 1, H = 512 1.9 us (2.6).
 // norm_any_kernel (chunks of 2 or 1 elements): what is wider than 14336, or whose width, stride or alignment is
-// not a multiple of 8. T = 8192: H = 7170 bf16 with residual 78 us, 7169 with 8-bit blocks 209 us, bound by
+// not a multiple of 8. T = 8192: H = 7170 bf16 with residual 78 us, 7169 with 8-bit blocks 212 us, bound by
 // the number of its 1- and 2-byte accesses. Where all three can run, in elements, pairs and by the kernels above:
-// H = 7168 196, 102, 88 us, H = 1024 22.4, 22.7, 13.2, T = 1 of 7168 5.4, 4.3, 3.3.
+// H = 7168 200, 105, 87 us, H = 1024 23.2, 23.6, 13.3, T = 1 of 7168 5.6, 4.7, 3.3. Elements of rows wider than 16384
+// (32 per thread of 1,024) are the one instance whose values do not fit its registers: some 500 bytes spill.
 
 __device__ __forceinline__ uint4 load16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 
@@ -699,7 +702,9 @@ __device__ __forceinline__ bool cache_row(const moe_rotary_args& a, int p_shift,
 // Every element is read and written once, so memory bounds it: N = 8192, 96 + 2 x 8 heads of 128, bf16:
 // 72.0 us, 6.5 TB/s, and 93 in pieces of 4, 296 of 1; with 104 of 128 rotated in halves, which need pieces of 4,
 // 107. U items per thread and blocks per SM measured there: 4 and 3 72.0, 4 and 4 (spills)
-// 87.5, 2 and 4 78.0, 2 and 6 77.4, 1 and 8 77.4 us; one item after another with two barriers per token 84 us.
+// 87.5, 2 and 4 78.0, 2 and 6 77.4, 1 and 8 77.4 us; one item after another with two barriers per token 84 us. (1 and 8,
+// and 2 and 6, which take tokens and calls of few items, spill 12 to 56 bytes too and are the faster there: N = 1531, 24 + 2 x 4
+// heads of 64 4.8 us, with 4 and 3 6.3.)
 template <int DT, bool INTER, int PE, int U, int MINB>
 __global__ void __launch_bounds__(kRotaryThreads, MINB) rotary_kernel(const moe_rotary_args a, int p_shift) {
   constexpr bool kInPiece = INTER && PE > 1;  // both elements of a pair lie in the piece
