@@ -2,7 +2,8 @@
  * moe_ops_gb300.h -- C ABI of the operators that stand beside the routed expert layer in a
  * decoder layer: the residual norm before attention and before the router, a serving step's
  * plan (positions, page tables, cache slots), rotary positions with the append to a paged
- * key/value cache, and attention of each request's new tokens over its pages.
+ * key/value cache, attention of each request's new tokens over its pages, drafted trees of
+ * tokens (plan, attention, acceptance), and 8-bit projections (quantisation, product).
  *
  * Conventions are those of moe_gb300.h: MOE_OK or a negative moe_status, argument errors
  * detected on the host before anything is enqueued, streams as void* of the current device
@@ -174,6 +175,126 @@ MOE_API int moe_attn_get_error(moe_attn_ctx* ctx, uint32_t* bits);
 /* Device bytes of the handle's workspace. */
 MOE_API int64_t moe_attn_device_bytes(const moe_attn_ctx* ctx);
 MOE_API int moe_attn_destroy(moe_attn_ctx* ctx);
+
+/* ---- drafted tokens ------------------------------------------------------------------------
+ * A step may bring a tree of drafted tokens for a request: its new tokens are the tree's nodes,
+ * every node behind its parent, appended to the cache in that order. Node t's parent is
+ * parents[q_start[b] + t], the parent's place in the request, or -1 where it follows the
+ * cached tokens. A node sees the cached tokens, its ancestors and itself. */
+
+/* Positions and masks of the nodes, once per step for all layers:
+ *   depth[t] = parent < 0 ? 0 : depth[parent] + 1        positions[n] = ctx_lens[b] + depth
+ *   mask[n]: bit j (bit j % 32 of word j / 32) is set where node t sees node j
+ * parents [N], mask [N][words], positions [N]. A request with more than 32 * words new tokens
+ * is a chunk without a tree: its parents have to be a chain (node t's is t - 1), its positions are
+ * ctx + t, and its mask is neither written here nor read by moe_attn_forward_tree, which lets its
+ * tokens see what is before them. A parent outside [-1, t), a longer request that is no chain, or a
+ * negative context raises MOE_OPS_ERR_PLAN and counts as -1, as a chain, as 0; a request whose
+ * rows lie outside [0, N] raises MOE_OPS_ERR_INDEX and is skipped. Rows of no request are not
+ * written. No output shares a word with an input or another output. 1 <= words <= MOE_TREE_WORDS. */
+#define MOE_TREE_WORDS 8
+typedef struct {
+  const int32_t* parents;
+  const int32_t* q_start;
+  const int32_t* ctx_lens;
+  int32_t* positions;
+  int32_t* mask;
+  uint32_t* err;
+  int32_t N, B, words;
+} moe_tree_plan_args;
+MOE_API int moe_tree_plan(void* stream, const moe_tree_plan_args* a);
+
+/* moe_attn_forward for requests with trees: of a request with at most 32 * words new tokens,
+ * row t sees the c = kv_lens - new cached keys and new key j where bit j of mask[n] is set (any
+ * bits: a row need not see itself, bits from the number of new tokens on are ignored); of a longer one
+ * it sees keys j <= c + t. A row that sees nothing gets zeros and lse = -inf. mask int32
+ * [N][words]; everything else as in moe_attn_forward. */
+MOE_API int moe_attn_forward_tree(moe_attn_ctx* ctx, void* stream, const moe_attn_args* a, const int32_t* mask,
+                                  int32_t words);
+
+/* The drafted tokens that the model's own tokens confirm, and their keys and values moved to the
+ * places that the next step expects. tokens[n] is a node's token, targets[n] the token that the
+ * model gives after it. The first c = certain[b] nodes of a request (1 where certain is NULL: the
+ * root, decided by the step before) are a chain that stays in any case; then from cur = c - 1
+ *   child = the lowest j > cur, j >= c, with parents[j] == cur and tokens[j] == targets[cur]
+ * is taken while there is one, at most `depth` times:
+ *   path[b][i] = the i-th node taken (-1 behind the last)      accepted[b] = c + nodes taken
+ *   ctx_out[b] = ctx_lens[b] + accepted[b]                     next_tokens[b] = targets[cur]
+ * and row ctx + path[b][i] of the caches goes to row ctx + c + i, in all layers. Other rows stay.
+ * A request without new tokens has accepted 0 and next_tokens -1. tokens, targets [N], path
+ * [B][depth]; a cache is [layers][pages][page_size][Hkv][D] of 16-bit elements with strides.
+ * certain outside [1, new] raises MOE_OPS_ERR_PLAN and is clamped; a row whose page is outside
+ * [0, num_pages) or whose place is outside the table raises MOE_OPS_ERR_INDEX and is not moved; a
+ * request whose rows lie outside [0, N] raises it and counts as without new tokens. No output
+ * shares a word with an input or another output; k_cache and v_cache share no element; a page
+ * belongs to one request. 1 <= depth <= 32 * MOE_TREE_WORDS, layers >= 1, B <= 65535,
+ * P a power of two, W * P < 2^31. */
+typedef struct {
+  const int32_t* parents;
+  const int32_t* tokens;
+  const int32_t* targets;
+  const int32_t* q_start;
+  const int32_t* ctx_lens;
+  const int32_t* certain;
+  const int32_t* block_table;
+  void* k_cache;
+  void* v_cache;
+  int32_t* path;
+  int32_t* accepted;
+  int32_t* ctx_out;
+  int32_t* next_tokens;
+  uint32_t* err;
+  int64_t table_stride;
+  int64_t kc_layer, kc_page, kc_row, kc_head, vc_layer, vc_page, vc_row, vc_head;
+  int32_t N, B, W, depth, layers, Hkv, D, page_size, num_pages;
+} moe_tree_accept_args;
+MOE_API int moe_tree_accept(void* stream, const moe_tree_accept_args* a);
+
+/* ---- 8-bit projections ----------------------------------------------------------------------
+ * Values in e4m3 with fp32 scales, s = max|x| / 448 over each block:
+ *   out8 = e4m3(x / s), the quotient in fp32, rounded to nearest even
+ * rows 1: blocks of `group` = 128 consecutive elements of a row, or the row (group 0); rows 128
+ * (with group 128): blocks of 128 x 128, as moe_matmul8_forward takes weights. Blocks at the ends may be
+ * smaller. scales [ceil(T / rows)][ceil(H / group)], contiguous. A block of zeros has s = 0 and zeros; a NaN
+ * makes its block's scale and values NaN; an infinity its scale infinite, itself NaN and the
+ * others 0. x [T][H] of dtype, out8 [T][H], rows strided; out8 and scales share no byte with x or
+ * one another. */
+typedef struct {
+  const void* x;
+  uint8_t* out8;
+  float* scales;
+  int64_t x_stride, out8_stride;
+  int32_t T, H, dtype, group, rows;
+} moe_quantize8_args;
+MOE_API int moe_quantize8(void* stream, const moe_quantize8_args* a);
+
+/* Product of e4m3 activations and weights with scales per block of 128 along K:
+ *   out[t][n] = sum_b a_scales[t][b] * w_scales[n / 128][b] * sum_{k in block b} a8[t][k] w8[n][k]
+ * The products of a block are summed by the tensor cores in fp32, the blocks in fp32; out is rounded once to
+ * dtype. a8 [T][K], w8 [N][K] (a library layer's [out][in]), out [T][N]; w_scales
+ * [ceil(N / 128)][ceil(K / 128)]; a_scales [T][a_blocks], a_blocks = ceil(K / 128), or 1 for a
+ * scale per row. The scales are as moe_add_rmsnorm (group 0, 128) and moe_quantize8 write them;
+ * rows of every tensor may be strided. K a multiple of 16, a8 and w8 16-byte aligned with row strides that
+ * are multiples of 16; out is aligned to its elements and shares no byte with an input.
+ * T, N >= 0; T or N 0: nothing is done. K >= 16. */
+typedef struct {
+  const uint8_t* a8;
+  const float* a_scales;
+  const uint8_t* w8;
+  const float* w_scales;
+  void* out;
+  int64_t a8_stride, a_scales_stride, w8_stride, w_scales_stride, out_stride;
+  int32_t T, N, K, a_blocks, dtype;
+} moe_matmul8_args;
+
+typedef struct moe_matmul8_ctx moe_matmul8_ctx; /* opaque: device workspace and error word */
+
+/* Handle, error word and workspace: as moe_attn_create and the calls behind it. */
+MOE_API int moe_matmul8_create(int device, moe_matmul8_ctx** out);
+MOE_API int moe_matmul8_forward(moe_matmul8_ctx* ctx, void* stream, const moe_matmul8_args* a);
+MOE_API int moe_matmul8_get_error(moe_matmul8_ctx* ctx, uint32_t* bits);
+MOE_API int64_t moe_matmul8_device_bytes(const moe_matmul8_ctx* ctx);
+MOE_API int moe_matmul8_destroy(moe_matmul8_ctx* ctx);
 
 #ifdef __cplusplus
 }

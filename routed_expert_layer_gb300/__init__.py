@@ -20,7 +20,8 @@ _CSRC = os.path.join(_HERE, "csrc")
 _BUILD = os.path.join(_HERE, "_build")
 LIB_PATH = os.path.join(_BUILD, "libmoe_gb300.so")
 BINDING_PATH = os.path.join(_BUILD, "_ops_binding.so")  # CPython binding of the operators in ops.py
-_SOURCES = ["api.cu", "route.cu", "router_tc.cu", "expert_tc.cu", "noalloc.cu", "block.cu", "ops.cu", "attn.cu"]
+_SOURCES = ["api.cu", "route.cu", "router_tc.cu", "expert_tc.cu", "noalloc.cu", "block.cu", "ops.cu", "attn.cu", "tree.cu",
+            "matmul8.cu"]
 _HEADERS = ["moe_internal.cuh", "tc_ptx.cuh", "ops_internal.cuh"]
 _INCLUDES = ["moe_gb300.h", "moe_ops_gb300.h"]
 NVCC_ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -37,7 +38,9 @@ EXPORTED = ["moe_create", "moe_load_layer", "moe_forward", "moe_forward_host", "
             "moe_profile_stage_name", "moe_profile_begin", "moe_profile_end", "moe_device_bytes", "moe_launch_count",
             "moe_route_noalloc", "moe_plan", "moe_forward_routed", "moe_debug_pdl_copy",
             "moe_add_rmsnorm", "moe_paged_plan", "moe_rotary_append", "moe_attn_create", "moe_attn_forward",
-            "moe_attn_get_error", "moe_attn_device_bytes", "moe_attn_destroy"]
+            "moe_attn_get_error", "moe_attn_device_bytes", "moe_attn_destroy", "moe_attn_forward_tree", "moe_tree_plan",
+            "moe_tree_accept", "moe_quantize8", "moe_matmul8_create", "moe_matmul8_forward", "moe_matmul8_get_error",
+            "moe_matmul8_device_bytes", "moe_matmul8_destroy"]
 
 # Revision of each kernel's code; a stored ncu traffic figure is only reported while
 # the revision it was measured on is current. "gateup" and "down" are the decode grouped
@@ -165,6 +168,16 @@ def lib():
         L.moe_attn_device_bytes.restype = ctypes.c_int64
         L.moe_attn_device_bytes.argtypes = [vp]
         L.moe_attn_destroy.argtypes = [vp]
+        L.moe_attn_forward_tree.argtypes = [vp, vp, p, p, i32]
+        L.moe_tree_plan.argtypes = [vp, p]
+        L.moe_tree_accept.argtypes = [vp, p]
+        L.moe_quantize8.argtypes = [vp, p]
+        L.moe_matmul8_create.argtypes = [ctypes.c_int, ctypes.POINTER(vp)]
+        L.moe_matmul8_forward.argtypes = [vp, vp, p]
+        L.moe_matmul8_get_error.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
+        L.moe_matmul8_device_bytes.restype = ctypes.c_int64
+        L.moe_matmul8_device_bytes.argtypes = [vp]
+        L.moe_matmul8_destroy.argtypes = [vp]
         _lib = L
     return _lib
 
@@ -446,7 +459,8 @@ class MoeLayer:
             pass
 
 
-_OPS = ("add_rmsnorm", "paged_plan", "rope_frequencies", "rotary_append", "PagedAttention")
+_OPS = ("add_rmsnorm", "paged_plan", "rope_frequencies", "rotary_append", "PagedAttention", "tree_plan", "tree_accept",
+        "quantize8", "Matmul8")
 
 
 def __getattr__(name):

@@ -104,14 +104,17 @@ struct AttnParams {
   int tpt;         // tokens per tile
   int box_tok;     // tokens per Q box
   float scale_log2;
+  const uint32_t* mask;  // [N][words] of new tokens a row sees (TREE)
+  int words;
   uint32_t* err;
   int32_t* tickets;  // [CTAs][QT][3], zero between calls: finished pieces (or runs) of the split item that starts in
                      // the CTA, of that item's first run, and of the run of an earlier item that starts in the CTA
   float* parts;      // [2 CTAs][QT] partial results: O [D/4][128][4], m [128], l [128], m and l of a joined run
 };
 
-template <int DT_, int D_, int QT_, int BN_, int NK_, int NV_>
+template <int DT_, int D_, int QT_, int BN_, int NK_, int NV_, bool TREE_>
 struct AttnCfg {
+  static constexpr bool TREE = TREE_;
   static constexpr int DT = DT_, D = D_, QT = QT_, BN = BN_, NK = NK_, NV = NV_;
   static constexpr int kThreads = 128 + 128 * QT;
   static constexpr int kCtasPerSm = QT == 1 ? 2 : 1;
@@ -223,21 +226,39 @@ struct Work {
   }
 };
 
+// Whether the request's new tokens see one another by their masks (else in a row, as in all calls without masks).
+template <bool TREE>
+__device__ __forceinline__ bool by_mask(const AttnParams& p, const Work& w) {
+  return TREE && w.n_new <= 32 * p.words;
+}
+
+// Which of 32 new tokens a row with these mask words sees, the first of them `rel` (cached tokens lie below 0: all seen).
+__device__ __forceinline__ uint32_t mask_bits(const uint32_t* row, int words, int n_new, int rel) {
+  const auto word = [&](int i) {
+    if (i < 0) return 0xFFFFFFFFu;
+    const int left = n_new - 32 * i;
+    if (i >= words || left <= 0) return 0u;
+    return left < 32 ? row[i] & ((1u << left) - 1u) : row[i];
+  };
+  return __funnelshift_r(word(rel >> 5), word((rel >> 5) + 1), rel & 31);
+}
+
 // The part of an item that is a CTA's. A boundary between two stretches counts as the item's start
 // where it lies in the item's first tile or before, and anywhere in an item that is not split.
-template <int QT, int BN>
+template <int QT, int BN, bool TREE>
 struct Piece {
   int t0, t1;      // tiles of BN keys
   int tq1[QT];     // the end for each row tile (its own last visible key)
   int kv_end;      // keys visible to the item's last row
-  int first_lim;   // keys visible to its first row
+  int first_lim;   // keys visible to its first row (with masks: to every row)
   int64_t first_part;  // the length of axis in which a boundary counts as the start
   bool none;       // nothing of the item is this CTA's
   bool split;
   __device__ __forceinline__ Piece(const AttnParams& p, const Work& w, const Axis& ax) {
     const int tok = w.i * QT * p.tpt;
-    kv_end = max(0, w.ctx + min(tok + QT * p.tpt, w.n_new));
-    first_lim = w.ctx + tok + 1;
+    const bool tree = by_mask<TREE>(p, w);
+    kv_end = max(0, w.ctx + (tree ? w.n_new : min(tok + QT * p.tpt, w.n_new)));
+    first_lim = tree ? max(w.ctx, 0) : w.ctx + tok + 1;
     const int nt = (kv_end + BN - 1) / BN;
     first_part = w.cost <= max(ax.whole, (int64_t)w.fixed + BN) ? w.cost : w.fixed + BN;
     int64_t lo = max(ax.x0 - w.at, (int64_t)0), hi = min(ax.x1 - w.at, w.cost);
@@ -249,7 +270,7 @@ struct Piece {
     t1 = none ? t0 : hi == w.cost ? nt : (int)min((int64_t)nt, max(hi - w.fixed, (int64_t)0) / BN);
 #pragma unroll
     for (int q = 0; q < QT; ++q) {
-      const int end = tok + q * p.tpt < w.n_new ? max(0, w.ctx + min(tok + (q + 1) * p.tpt, w.n_new)) : 0;
+      const int end = tok + q * p.tpt >= w.n_new ? 0 : tree ? kv_end : max(0, w.ctx + min(tok + (q + 1) * p.tpt, w.n_new));
       tq1[q] = min(t1, (end + BN - 1) / BN);
     }
   }
@@ -325,6 +346,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
     attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v, const __grid_constant__ AttnParams p) {
   constexpr int D = C::D, QT = C::QT, BN = C::BN, NK = C::NK, NV = C::NV, DT = C::DT;
+  constexpr bool TREE = C::TREE;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* sq = smem;
@@ -431,7 +453,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
     const int rows = P >= BN ? BN : P;  // keys per box
     uint32_t kn = 0, vn = 0, qn = 0;
     while (more) {
-      const Piece<QT, BN> pc(p, w, ax);
+      const Piece<QT, BN, TREE> pc(p, w, ax);
       if (pc.tiles()) {
         if (!warp_wait(qempty, (qn & 1) ^ 1u, p.err)) {
           ok = false;
@@ -526,7 +548,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
       const auto wait_k = [&] { return mbar_wait_suspended(&kfull[kn % NK], (kn / NK) & 1, p.err); };
       const auto wait_v = [&](uint32_t n) { return mbar_wait_suspended(&vclean[n % NV], (n / NV) & 1, p.err); };
       while (more) {
-        const Piece<QT, BN> pc(p, w, ax);
+        const Piece<QT, BN, TREE> pc(p, w, ax);
         if (pc.tiles()) {
           ok = mbar_wait_suspended(qfull, pn & 1, p.err) && wait_k();
           if (!ok) break;
@@ -593,7 +615,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
     const int cw = warp - 2;
     uint32_t vn = 0, pn = 0;
     while (more) {
-      const Piece<QT, BN> pc(p, w, ax);
+      const Piece<QT, BN, TREE> pc(p, w, ax);
       if (pc.tiles()) {
         uint32_t* note = notes + (pn % kNoteSlots) * 16 + cw * 8;
         if (lane < 8) note[lane] = 0;
@@ -629,7 +651,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
                   if (hit) *u = val;
                   odd |= hit;
                 }
-              const int rel = (int)(key - pc.first_lim);  // < QT * tpt <= 256
+              const int rel = (int)(key - pc.first_lim);  // < QT * tpt <= 256 (with masks: < n_new <= 256)
               if (odd) atomicOr(&note[rel >> 5], 1u << (rel & 31));
             }
             fence_proxy_async();
@@ -661,7 +683,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
       int t0, t_end, lim, tile_lim;
       bool live, warp_live;
       {
-        const Piece<QT, BN> pc(p, w, ax);
+        const Piece<QT, BN, TREE> pc(p, w, ax);
         if (pc.none) {
           advance();
           continue;
@@ -671,8 +693,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         t_end = q == 0 ? pc.tq1[0] : pc.tq1[QT - 1];
         live = rt < n_tok;
         warp_live = quarter * 32 < n_tok * p.G;
-        lim = w.ctx + tok + rt + 1;   // keys this row sees (live rows)
-        tile_lim = w.ctx + tok + 1;   // keys every row of the tile sees
+        const bool tree = by_mask<TREE>(p, w);
+        lim = tree ? pc.kv_end : w.ctx + tok + rt + 1;       // keys this row sees, or may see by its mask (live rows)
+        tile_lim = tree ? pc.first_lim : w.ctx + tok + 1;   // keys every row of the tile sees
       }
       __syncwarp();
       if (lane == 0) *place = w;
@@ -687,15 +710,35 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
           const int64_t key0 = (int64_t)t * BN;
           if (key0 + BN > tile_lim) {  // hide keys in place: few tiles need it, so it is kept out of the code of the others
             const int see = (int)max(min((int64_t)lim - key0, (int64_t)BN), (int64_t)0);
+            if constexpr (TREE) {  // what the masks need waits in the parked place
+              const int n_new = place->n_new, rel0 = (int)key0 - place->ctx;
+              const bool tree = live && n_new <= 32 * p.words;
+              const uint32_t* row = p.mask + (int64_t)(place->q0 + (place->i * QT + q) * p.tpt + rt) * p.words;
 #pragma unroll 1
-            for (int c = 0; c < BN; c += 32) {
-              uint32_t v[32];
-              tmem_ld32(ts + c, v);
-              tmem_wait_ld32(v);
+              for (int c = 0; c < BN; c += 32) {
+                const int left = see - c;
+                const uint32_t bits = tree ? mask_bits(row, p.words, n_new, rel0 + c)
+                                           : left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1u;
+                uint32_t v[32];
+                __syncwarp();
+                tmem_ld32(ts + c, v);
+                tmem_wait_ld32(v);
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (c + k >= see) v[k] = 0xFF800000u;  // -inf
-              tmem_st32(ts + c, v);
+                for (int k = 0; k < 32; ++k)
+                  if (!(bits >> k & 1)) v[k] = 0xFF800000u;  // -inf
+                tmem_st32(ts + c, v);
+              }
+            } else {
+#pragma unroll 1
+              for (int c = 0; c < BN; c += 32) {
+                uint32_t v[32];
+                tmem_ld32(ts + c, v);
+                tmem_wait_ld32(v);
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (c + k >= see) v[k] = 0xFF800000u;  // -inf
+                tmem_st32(ts + c, v);
+              }
             }
             tmem_wait_st();
           }
@@ -761,7 +804,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
       // ---- the piece's result: to out, or to the workspace where the item is split ----
       const bool any = t0 < t_end;
       w = *place;
-      const Piece<QT, BN> pc(p, w, *parked_axis);
+      const Piece<QT, BN, TREE> pc(p, w, *parked_axis);
       const int tok = (w.i * QT + q) * p.tpt;       // the tile's first token
       const int n_tok = min(p.tpt, w.n_new - tok);  // its tokens (<= 0: no such tile)
       if (pc.tiles()) {
@@ -802,6 +845,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
               for (int rel = 0; rel < lim - pc.first_lim; ++rel) {
                 if (!((note[rel >> 5] | note[8 + (rel >> 5)]) >> (rel & 31) & 1)) continue;
                 const int key = pc.first_lim + rel, col = key >> p.p_shift;
+                if constexpr (TREE) {
+                  if (by_mask<TREE>(p, w) && !(mask_bits(p.mask + n_row * p.words, p.words, w.n_new, key - w.ctx) & 1)) continue;
+                }
                 const int id = p.a.block_table[w.b * p.a.table_stride + col];
                 const uint16_t* v = (const uint16_t*)p.a.v_cache + id * p.a.vc_page +
                                     (key & (p.a.page_size - 1)) * p.a.vc_row + w.h * p.a.vc_head + c;
@@ -1007,10 +1053,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
   }
 }
 
-template <int DT, int D>
-using StreamCfg = AttnCfg<DT, D, 1, 64, 2, 2>;
-template <int DT, int D>
-using ChunkCfg = AttnCfg<DT, D, 2, 128, 2, 2>;
+template <int DT, int D, bool TREE>
+using StreamCfg = AttnCfg<DT, D, 1, 64, 2, 2, TREE>;
+template <int DT, int D, bool TREE>
+using ChunkCfg = AttnCfg<DT, D, 2, 128, 2, 2, TREE>;
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -1045,8 +1091,13 @@ bool make_map(CUtensorMap* map, const void* base, int dt, int rank, const int64_
 }
 
 template <class C>
-cudaError_t attn_configure() {
-  return cudaFuncSetAttribute(attn_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+bool attn_configure() {
+  return cudaFuncSetAttribute(attn_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem) == cudaSuccess;
+}
+template <int DT, int D>
+bool attn_configure_all() {
+  return attn_configure<StreamCfg<DT, D, false>>() && attn_configure<ChunkCfg<DT, D, false>>() &&
+         attn_configure<StreamCfg<DT, D, true>>() && attn_configure<ChunkCfg<DT, D, true>>();
 }
 
 template <class C>
@@ -1067,11 +1118,15 @@ int attn_launch(const moe_attn_ctx* ctx, const AttnParams& p, cudaStream_t s) {
              : MOE_ERR_CUDA;
 }
 
-template <int DT, int D>
+template <int DT, int D, bool TREE>
 int attn_by_rows(const moe_attn_ctx* ctx, const AttnParams& p, cudaStream_t s) {
   const int64_t most = p.a.max_new > 0 ? std::min(p.a.max_new, p.a.N) : p.a.N;
-  if (most <= p.tpt) return attn_launch<StreamCfg<DT, D>>(ctx, p, s);
-  return attn_launch<ChunkCfg<DT, D>>(ctx, p, s);
+  if (most <= p.tpt) return attn_launch<StreamCfg<DT, D, TREE>>(ctx, p, s);
+  return attn_launch<ChunkCfg<DT, D, TREE>>(ctx, p, s);
+}
+template <int DT, int D>
+int attn_by_mask(const moe_attn_ctx* ctx, const AttnParams& p, cudaStream_t s) {
+  return p.mask ? attn_by_rows<DT, D, true>(ctx, p, s) : attn_by_rows<DT, D, false>(ctx, p, s);
 }
 
 // Clears the error word and the tickets. cudaMemset does not wait, and streams that do not wait for the default one
@@ -1127,6 +1182,30 @@ int attn_check(const moe_attn_args* a) {
   return MOE_OK;
 }
 
+int attn_forward(moe_attn_ctx* ctx, void* stream, const moe_attn_args* a, const int32_t* mask, int32_t words) {
+  DeviceGuard g(ctx->device);
+  AttnParams p;
+  p.a = *a;
+  p.p_shift = __builtin_ctz((unsigned)a->page_size);
+  p.scale_log2 = a->scale * 1.44269504088896340736f;
+  p.mask = (const uint32_t*)mask;
+  p.words = words;
+  p.err = ctx->err;
+  p.tickets = ctx->tickets;
+  p.parts = ctx->parts;
+  p.G = a->Hq / a->Hkv;
+  // A Q box is a whole number of 8-row swizzle atoms where that fits in a tile, so boxes can be
+  // laid one behind the other; a tile is then a whole number of boxes.
+  p.box_tok = 8 / std::gcd(p.G, 8);
+  if (p.box_tok * p.G > kRows) p.box_tok = kRows / p.G;
+  p.tpt = kRows / (p.box_tok * p.G) * p.box_tok;
+  OpsPdl pdl;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (a->dtype == MOE_DT_BF16)
+    return a->D == 64 ? attn_by_mask<MOE_DT_BF16, 64>(ctx, p, s) : attn_by_mask<MOE_DT_BF16, 128>(ctx, p, s);
+  return a->D == 64 ? attn_by_mask<MOE_DT_F16, 64>(ctx, p, s) : attn_by_mask<MOE_DT_F16, 128>(ctx, p, s);
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -1152,7 +1231,7 @@ int moe_attn_create(int device, moe_attn_ctx** out) {
   const size_t most = 2 * (size_t)c->sm_count;
   const size_t head = (256 + most * 3 * 4 + 255) / 256 * 256;
   c->head_bytes = head;
-  c->bytes = head + 2 * most * sizeof(float) * StreamCfg<0, 128>::kPart;
+  c->bytes = head + 2 * most * sizeof(float) * StreamCfg<MOE_DT_BF16, 128, false>::kPart;
   if (cudaMalloc(&c->mem, c->bytes) != cudaSuccess) {
     cudaGetLastError();
     delete c;
@@ -1161,11 +1240,8 @@ int moe_attn_create(int device, moe_attn_ctx** out) {
   c->err = (uint32_t*)c->mem;
   c->tickets = (int32_t*)((char*)c->mem + 256);
   c->parts = (float*)((char*)c->mem + head);
-  if (!clear_head(c) || attn_configure<StreamCfg<0, 64>>() != cudaSuccess ||
-      attn_configure<StreamCfg<0, 128>>() != cudaSuccess || attn_configure<StreamCfg<1, 64>>() != cudaSuccess ||
-      attn_configure<StreamCfg<1, 128>>() != cudaSuccess || attn_configure<ChunkCfg<0, 64>>() != cudaSuccess ||
-      attn_configure<ChunkCfg<0, 128>>() != cudaSuccess || attn_configure<ChunkCfg<1, 64>>() != cudaSuccess ||
-      attn_configure<ChunkCfg<1, 128>>() != cudaSuccess) {
+  if (!clear_head(c) || !attn_configure_all<MOE_DT_BF16, 64>() || !attn_configure_all<MOE_DT_BF16, 128>() ||
+      !attn_configure_all<MOE_DT_F16, 64>() || !attn_configure_all<MOE_DT_F16, 128>()) {
     cudaGetLastError();
     cudaFree(c->mem);
     delete c;
@@ -1179,25 +1255,17 @@ int moe_attn_forward(moe_attn_ctx* ctx, void* stream, const moe_attn_args* a) {
   if (!ctx) return MOE_ERR_INVALID_ARG;
   const int st = attn_check(a);
   if (st != MOE_OK || a->N == 0 || a->B == 0) return st;
-  DeviceGuard g(ctx->device);
-  AttnParams p;
-  p.a = *a;
-  p.p_shift = __builtin_ctz((unsigned)a->page_size);
-  p.scale_log2 = a->scale * 1.44269504088896340736f;
-  p.err = ctx->err;
-  p.tickets = ctx->tickets;
-  p.parts = ctx->parts;
-  p.G = a->Hq / a->Hkv;
-  // A Q box is a whole number of 8-row swizzle atoms where that fits in a tile, so boxes can be
-  // laid one behind the other; a tile is then a whole number of boxes.
-  p.box_tok = 8 / std::gcd(p.G, 8);
-  if (p.box_tok * p.G > kRows) p.box_tok = kRows / p.G;
-  p.tpt = kRows / (p.box_tok * p.G) * p.box_tok;
-  OpsPdl pdl;
-  cudaStream_t s = (cudaStream_t)stream;
-  if (a->dtype == MOE_DT_BF16)
-    return a->D == 64 ? attn_by_rows<MOE_DT_BF16, 64>(ctx, p, s) : attn_by_rows<MOE_DT_BF16, 128>(ctx, p, s);
-  return a->D == 64 ? attn_by_rows<MOE_DT_F16, 64>(ctx, p, s) : attn_by_rows<MOE_DT_F16, 128>(ctx, p, s);
+  return attn_forward(ctx, stream, a, nullptr, 0);
+}
+
+int moe_attn_forward_tree(moe_attn_ctx* ctx, void* stream, const moe_attn_args* a, const int32_t* mask, int32_t words) {
+  if (!ctx || words < 1) return MOE_ERR_INVALID_ARG;
+  const int st = attn_check(a);
+  if (st != MOE_OK) return st;
+  if (words > MOE_TREE_WORDS) return MOE_ERR_UNSUPPORTED;
+  if (a->N == 0 || a->B == 0) return MOE_OK;
+  if (!mask || !is_aligned(mask, 4)) return MOE_ERR_INVALID_ARG;
+  return attn_forward(ctx, stream, a, mask, words);
 }
 
 int moe_attn_get_error(moe_attn_ctx* ctx, uint32_t* bits) {

@@ -262,6 +262,20 @@ int rotary(PyObject* const* a) {
   return moe_rotary_append(stream_of(a[12], dev), &p);
 }
 
+// Which new tokens of its request a row sees: int32 [N][words], contiguous.
+struct Mask {
+  int32_t* bits;
+  int32_t words;
+  Mask(PyObject* o, const char* name, int64_t N, int dev) {
+    const at::Tensor& t = tensor(o, name);
+    if (t.dim() != 2) fail(PyExc_ValueError, std::string(name) + ": expected [N][words]");
+    expect(t, name, {N, t.size(1)}, at::kInt, dev);
+    if (!t.is_contiguous()) fail(PyExc_ValueError, std::string(name) + ": expected a contiguous tensor");
+    bits = static_cast<int32_t*>(ptr(t));
+    words = int32(t.size(1), name);
+  }
+};
+
 int attention(PyObject* const* a) {
   moe_attn_ctx* ctx = static_cast<moe_attn_ctx*>(PyLong_AsVoidPtr(a[0]));
   if (PyErr_Occurred()) throw Raised();
@@ -300,7 +314,141 @@ int attention(PyObject* const* a) {
   p.Hq = int32(q.size(1), "q");
   p.D = int32(q.size(2), "q");
   p.W = int32(table.size(1), "block_table");
-  return moe_attn_forward(ctx, stream_of(a[12], dev), &p);
+  if (a[13] == Py_None) return moe_attn_forward(ctx, stream_of(a[12], dev), &p);
+  const Mask tree(a[13], "tree", p.N, dev);
+  return moe_attn_forward_tree(ctx, stream_of(a[12], dev), &p, tree.bits, tree.words);
+}
+
+int tree_plan(PyObject* const* a) {
+  const at::Tensor& parents = tensor(a[0], "parents");
+  const int dev = device_of(parents, "parents");
+  const int64_t N = parents.numel(), B = tensor(a[2], "ctx_lens").numel();
+  moe_tree_plan_args p = {};
+  p.parents = ints(a[0], "parents", N, dev);
+  p.q_start = ints(a[1], "q_start", B + 1, dev);
+  p.ctx_lens = ints(a[2], "ctx_lens", B, dev);
+  p.positions = ints(a[3], "positions", N, dev);
+  const Mask mask(a[4], "mask", N, dev);
+  p.mask = mask.bits;
+  p.words = mask.words;
+  p.err = err_word(a[5], dev);
+  p.N = int32(N, "parents");
+  p.B = int32(B, "ctx_lens");
+  return moe_tree_plan(stream_of(a[6], dev), &p);
+}
+
+int tree_accept(PyObject* const* a) {
+  const at::Tensor& parents = tensor(a[0], "parents");
+  const int dev = device_of(parents, "parents");
+  const int64_t N = parents.numel(), B = tensor(a[4], "ctx_lens").numel();
+  moe_tree_accept_args p = {};
+  p.parents = ints(a[0], "parents", N, dev);
+  p.tokens = ints(a[1], "tokens", N, dev);
+  p.targets = ints(a[2], "targets", N, dev);
+  p.q_start = ints(a[3], "q_start", B + 1, dev);
+  p.ctx_lens = ints(a[4], "ctx_lens", B, dev);
+  const at::Tensor& table = tensor(a[5], "block_table");
+  if (table.dim() != 2) fail(PyExc_ValueError, "block_table: expected [B][W]");
+  p.table_stride = rows(table, "block_table", {B, table.size(1)}, at::kInt, dev);
+  p.block_table = static_cast<const int32_t*>(ptr(table));
+  const at::Tensor& k = tensor(a[6], "k_cache");
+  const at::Tensor& v = tensor(a[7], "v_cache");
+  const int64_t dims = k.dim();
+  if ((dims != 4 && dims != 5) || v.sizes() != k.sizes() || k.element_size() != 2 || !k.is_floating_point())
+    fail(PyExc_ValueError, "k_cache, v_cache: expected [pages][page_size][Hkv][D] or [layers][pages][page_size][Hkv][D] of 16-bit "
+                           "values, got " + list(k.sizes()) + ", " + list(v.sizes()));
+  expect(k, "k_cache", k.sizes(), k.scalar_type(), dev);
+  expect(v, "v_cache", k.sizes(), k.scalar_type(), dev);
+  const int64_t l = dims - 4;  // the first dimension behind the layers
+  p.layers = l ? int32(k.size(0), "k_cache") : 1;
+  p.kc_layer = l ? k.stride(0) : 0;
+  p.vc_layer = l ? v.stride(0) : 0;
+  p.num_pages = int32(k.size(l), "k_cache");
+  p.page_size = int32(k.size(l + 1), "k_cache");
+  p.Hkv = int32(k.size(l + 2), "k_cache");
+  p.D = int32(k.size(l + 3), "k_cache");
+  p.kc_page = k.stride(l);
+  p.kc_row = k.stride(l + 1);
+  p.kc_head = k.stride(l + 2);
+  p.vc_page = v.stride(l);
+  p.vc_row = v.stride(l + 1);
+  p.vc_head = v.stride(l + 2);
+  p.k_cache = ptr(k);
+  p.v_cache = ptr(v);
+  const at::Tensor& path = tensor(a[8], "path");
+  if (path.dim() != 2) fail(PyExc_ValueError, "path: expected [B][depth]");
+  expect(path, "path", {B, path.size(1)}, at::kInt, dev);
+  if (!path.is_contiguous()) fail(PyExc_ValueError, "path: expected a contiguous tensor");
+  p.path = static_cast<int32_t*>(ptr(path));
+  p.depth = int32(path.size(1), "path");
+  p.accepted = ints(a[9], "accepted", B, dev);
+  p.ctx_out = ints(a[10], "ctx_out", B, dev);
+  p.next_tokens = ints(a[11], "next_tokens", B, dev);
+  p.certain = a[12] == Py_None ? nullptr : ints(a[12], "certain", B, dev);
+  p.err = err_word(a[13], dev);
+  p.N = int32(N, "parents");
+  p.B = int32(B, "ctx_lens");
+  p.W = int32(table.size(1), "block_table");
+  return moe_tree_accept(stream_of(a[14], dev), &p);
+}
+
+const at::Tensor& bytes8(PyObject* o, const char* name) {
+  const at::Tensor& t = tensor(o, name);
+  if ((t.scalar_type() != at::kFloat8_e4m3fn && t.scalar_type() != at::kByte) || t.dim() != 2)
+    fail(PyExc_ValueError, std::string(name) + ": expected float8_e4m3fn or uint8, 2 dimensions, got " + at::toString(t.scalar_type()) +
+                               " " + list(t.sizes()));
+  return t;
+}
+
+int quantize8(PyObject* const* a) {
+  const at::Tensor& x = tensor(a[0], "x");
+  const int dev = device_of(x, "x");
+  moe_quantize8_args p = {};
+  p.dtype = dtype16(x, "x", 2, "[T][H]");
+  p.x_stride = rows(x, "x", x.sizes(), x.scalar_type(), dev);
+  p.x = ptr(x);
+  const int64_t T = x.size(0), H = x.size(1);
+  const at::Tensor& o = bytes8(a[1], "out8");
+  p.out8_stride = rows(o, "out8", x.sizes(), o.scalar_type(), dev);
+  p.out8 = static_cast<uint8_t*>(ptr(o));
+  p.group = int32(a[3], "group");
+  p.rows = int32(a[4], "rows");
+  const at::Tensor& s = tensor(a[2], "scales");
+  expect(s, "scales", {p.rows > 0 ? (T + p.rows - 1) / p.rows : T, p.group > 0 ? (H + p.group - 1) / p.group : 1}, at::kFloat, dev);
+  if (!s.is_contiguous()) fail(PyExc_ValueError, "scales: expected a contiguous tensor");
+  p.scales = static_cast<float*>(ptr(s));
+  p.T = int32(T, "x");
+  p.H = int32(H, "x");
+  return moe_quantize8(stream_of(a[5], dev), &p);
+}
+
+int matmul8(PyObject* const* a) {
+  moe_matmul8_ctx* ctx = static_cast<moe_matmul8_ctx*>(PyLong_AsVoidPtr(a[0]));
+  if (PyErr_Occurred()) throw Raised();
+  const int dev = int32(a[1], "device");  // the handle's
+  moe_matmul8_args p = {};
+  const at::Tensor& x = bytes8(a[2], "a8");
+  const at::Tensor& w = bytes8(a[4], "w8");
+  const int64_t T = x.size(0), K = x.size(1), N = w.size(0), blocks = (K + 127) / 128;
+  p.a8_stride = rows(x, "a8", {T, K}, x.scalar_type(), dev);
+  p.w8_stride = rows(w, "w8", {N, K}, w.scalar_type(), dev);
+  const at::Tensor& as = tensor(a[3], "a_scales");
+  p.a_blocks = as.dim() == 2 && as.size(1) == 1 ? 1 : int32(blocks, "a8");
+  p.a_scales_stride = rows(as, "a_scales", {T, p.a_blocks}, at::kFloat, dev);
+  const at::Tensor& ws = tensor(a[5], "w_scales");
+  p.w_scales_stride = rows(ws, "w_scales", {(N + 127) / 128, blocks}, at::kFloat, dev);
+  const at::Tensor& o = tensor(a[6], "out");
+  p.dtype = dtype16(o, "out", 2, "[T][N]");
+  p.out_stride = rows(o, "out", {T, N}, o.scalar_type(), dev);
+  p.a8 = static_cast<const uint8_t*>(ptr(x));
+  p.w8 = static_cast<const uint8_t*>(ptr(w));
+  p.a_scales = static_cast<const float*>(ptr(as));
+  p.w_scales = static_cast<const float*>(ptr(ws));
+  p.out = ptr(o);
+  p.T = int32(T, "a8");
+  p.N = int32(N, "w8");
+  p.K = int32(K, "a8");
+  return moe_matmul8_forward(ctx, stream_of(a[7], dev), &p);
 }
 
 // No C++ exception leaves a function.
@@ -323,7 +471,11 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 PyMethodDef methods[] = {{"norm", ENTRY(norm, 11), METH_FASTCALL, nullptr},
                          {"plan", ENTRY(plan, 13), METH_FASTCALL, nullptr},
                          {"rotary", ENTRY(rotary, 13), METH_FASTCALL, nullptr},
-                         {"attention", ENTRY(attention, 13), METH_FASTCALL, nullptr},
+                         {"attention", ENTRY(attention, 14), METH_FASTCALL, nullptr},
+                         {"tree_plan", ENTRY(tree_plan, 7), METH_FASTCALL, nullptr},
+                         {"tree_accept", ENTRY(tree_accept, 15), METH_FASTCALL, nullptr},
+                         {"quantize8", ENTRY(quantize8, 6), METH_FASTCALL, nullptr},
+                         {"matmul8", ENTRY(matmul8, 8), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

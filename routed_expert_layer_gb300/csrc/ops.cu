@@ -61,15 +61,6 @@ __device__ __forceinline__ void store_vec(uint16_t* p, const float (&v)[N]) {
   }
 }
 
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// |v| as an unsigned integer: its order is that of the magnitudes, and a NaN is the largest.
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-
 // The 8-bit output is y / s as y * (1 / s). Where s lies below fp32's normal range, 1 / s lies above its largest
 // value: there both y and s are taken kLift times larger first.
 constexpr float kLift = 0x1p64f;
@@ -465,24 +456,6 @@ __global__ void __launch_bounds__(TX < 256 ? 256 : TX, MINB) norm_any_kernel(con
   }
 }
 
-constexpr int kMaxDevices = 64;
-int current_device() {
-  int dev = 0;
-  return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices ? dev : 0;
-}
-
-// SMs of the current device (a constant of the device, read once for each).
-int sm_count() {
-  static int known[kMaxDevices];
-  const int dev = current_device();
-  if (!known[dev]) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 152;
-    known[dev] = n;
-  }
-  return known[dev];
-}
-
 template <int DT, int NV, int MAXT, int MINB>
 cudaError_t launch_norm_rows(const NormParams& p, cudaStream_t s) {
   const int tx = ((p.H / 8 + NV - 1) / NV + 31) / 32 * 32;
@@ -823,12 +796,6 @@ cudaError_t launch_rotary(const moe_rotary_args& a, int pe, int p_shift, cudaStr
                    : launch_rotary_pieces<DT, INTER, 1>(a, p_shift, s);
 }
 
-int shift_of(int p) {
-  int s = 0;
-  while ((1 << s) < p) ++s;
-  return s;
-}
-
 }  // namespace
 }  // namespace moe
 
@@ -897,25 +864,18 @@ int moe_paged_plan(void* stream, const moe_paged_plan_args* a) {
   if (a->B > MOE_PLAN_MAX_REQUESTS || (int64_t)a->W * a->page_size >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
   // Every block reads the inputs again after others have begun to write: an output that shares a word with an
   // input, or with another output, would change positions, slots and table columns, or write past the table.
-  struct {
-    const void* p;
-    int64_t words;
-  } const t[] = {{a->block_table, (a->B - 1) * a->table_stride + a->W},
-                 {a->q_start, (int64_t)a->B + 1},
-                 {a->kv_lens, a->B},
-                 {a->positions, a->N},
-                 {a->slots, a->N},
-                 {a->free_head_out, 1},
-                 {a->err, a->err ? 1 : 0},  // outputs up to here
-                 {a->ctx_lens, a->B},
-                 {a->new_lens, a->B},
-                 {a->free_pages, a->F},
-                 {a->free_head, 1}};
-  for (int o = 0; o < 7; ++o)
-    for (int i = o + 1; i < 11; ++i) {
-      const uintptr_t x = (uintptr_t)t[o].p, y = (uintptr_t)t[i].p;
-      if (x < y + 4 * t[i].words && y < x + 4 * t[o].words && t[o].words && t[i].words) return MOE_ERR_INVALID_ARG;
-    }
+  const Words t[] = {{a->block_table, (a->B - 1) * a->table_stride + a->W},
+                     {a->q_start, (int64_t)a->B + 1},
+                     {a->kv_lens, a->B},
+                     {a->positions, a->N},
+                     {a->slots, a->N},
+                     {a->free_head_out, 1},
+                     {a->err, a->err ? 1 : 0},  // outputs up to here
+                     {a->ctx_lens, a->B},
+                     {a->new_lens, a->B},
+                     {a->free_pages, a->F},
+                     {a->free_head, 1}};
+  if (shares_words(t, 7, 11)) return MOE_ERR_INVALID_ARG;
   const int blocks = (a->N + kPlanThreads - 1) / kPlanThreads;
   OpsPdl pdl;
   return launch_pdl(plan_kernel, dim3((unsigned)(blocks < 1 ? 1 : blocks > 304 ? 304 : blocks)), dim3(kPlanThreads),

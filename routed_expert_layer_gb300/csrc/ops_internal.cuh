@@ -1,4 +1,4 @@
-// Helpers shared by the operators beside the expert layer (ops.cu, attn.cu): 16-bit types,
+// Helpers shared by the operators beside the expert layer (ops.cu, attn.cu, tree.cu, matmul8.cu): 16-bit types,
 // host-side checks, launches.
 #pragma once
 
@@ -39,6 +39,16 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Two fp32 to e4m3, rounded to nearest even, beyond 448 saturated (low byte first).
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// |v| as an unsigned integer: its order is that of the magnitudes, and a NaN is the largest.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
 inline bool is_aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 inline bool is_pow2(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
 
@@ -63,6 +73,45 @@ struct DeviceGuard {
     if (prev >= 0) cudaSetDevice(prev);
   }
 };
+
+constexpr int kMaxDevices = 64;
+inline int current_device() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices ? dev : 0;
+}
+
+// SMs of the current device (a constant of the device, read once for each).
+inline int sm_count() {
+  static int known[kMaxDevices];
+  const int dev = current_device();
+  if (!known[dev]) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 152;
+    known[dev] = n;
+  }
+  return known[dev];
+}
+
+inline int shift_of(int p) {
+  int s = 0;
+  while ((1 << s) < p) ++s;
+  return s;
+}
+
+// Words of an output or input of a call, for finding outputs that share memory with another tensor of it.
+struct Words {
+  const void* p;
+  int64_t n;
+};
+// Whether one of the first `outputs` tensors shares a word with another tensor.
+inline bool shares_words(const Words* t, int outputs, int count) {
+  for (int o = 0; o < outputs; ++o)
+    for (int i = o + 1; i < count; ++i) {
+      const uintptr_t x = (uintptr_t)t[o].p, y = (uintptr_t)t[i].p;
+      if (x < y + 4 * t[i].n && y < x + 4 * t[o].n && t[o].n && t[i].n) return true;
+    }
+  return false;
+}
 
 // Programmatic dependent launch for the launches of one operator call.
 struct OpsPdl {
