@@ -1058,22 +1058,11 @@ using StreamCfg = AttnCfg<DT, D, 1, 64, 2, 2, TREE>;
 template <int DT, int D, bool TREE>
 using ChunkCfg = AttnCfg<DT, D, 2, 128, 2, 2, TREE>;
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 // A tensor of 16-bit elements read in boxes with 128-byte swizzle; dims innermost first,
 // strides (elements) of the outer dimensions. Host-only, so it may run during stream capture.
 bool make_map(CUtensorMap* map, const void* base, int dt, int rank, const int64_t* dims, const int64_t* strides,
               const int* box) {
-  static const EncodeTiledFn encode = [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      fn = nullptr;
-    return reinterpret_cast<EncodeTiledFn>(fn);
-  }();
+  const TensorMapFn encode = tensor_map_fn();
   if (!encode) return false;
   cuuint64_t d[4], s[3];
   cuuint32_t b[4], e[4];

@@ -2,8 +2,6 @@
 // (interfaces and formulas: include/moe_ops_gb300.h).
 #include <algorithm>
 
-#include <cuda_fp8.h>
-
 #include "ops_internal.cuh"
 #include "tc_ptx.cuh"
 
@@ -12,7 +10,10 @@ struct moe_matmul8_ctx {
   int sm_count = 0;
   void* mem = nullptr;
   size_t bytes = 0;
+  size_t head_bytes = 0;  // error word and tickets
   uint32_t* err = nullptr;
+  int32_t* tickets = nullptr;
+  float* parts = nullptr;
 };
 
 namespace moe {
@@ -55,58 +56,420 @@ __global__ void __launch_bounds__(256) quantize_kernel(const moe_quantize8_args 
 }
 
 // ---- product -----------------------------------------------------------------------------------
+//
+// D (128 x BN per CTA, tokens in tensor memory's lanes) = A8 W8^T of one block of 128 along K, on the tensor cores; the
+// epilogue warps multiply it by the block's two scales into fp32 registers while the next block's product
+// is computed into another part of tensor memory: acc += (a_scale w_scale) D, one operation an element.
+//
+// Two instances. Up to 128 tokens one CTA takes 128 rows of W8 and all tokens, so the weights are read once: it streams
+// them. More tokens: a pair of CTAs takes 256 tokens and 256 rows of W8; its MMA reads each CTA's half of W8's
+// rows from that CTA's shared memory, so each CTA loads 128 rows of A8 and 128 of W8 for 128 x 256 outputs.
+//
+// Work. A unit is a block of 128 of a tile. Whole rounds of tiles over all CTAs (or pairs) go tile by tile; the tiles
+// left over, all of a small product, are laid on one axis of units and cut into equal stretches. The
+// pieces of a tile go through the workspace and the warp that finishes last adds them in K's order (so results
+// do not depend on which one that was), for its own 32 rows and 128 columns: no warp waits for another.
+//
+// Warps. 0: TMA (a box of A8 and one of W8 per unit). 1: issues the MMAs (of a pair: the first CTA's). 2..: epilogue, a
+// thread per row, 128 columns each.
 
-constexpr int kTile = 64;
+using namespace ptx;
 
-// 64 x 64 outputs per block, 4 x 4 per thread, values as fp32 in shared memory.
-template <int DT>
-__global__ void __launch_bounds__(256) matmul8_kernel(const moe_matmul8_args a) {
-  __shared__ float sa[32][kTile + 1], sw[32][kTile + 1];
+constexpr int kMinUnits = 4;  // units of a stretch at least
+
+struct MatmulParams {
+  moe_matmul8_args a;
+  int kb;                  // units of a tile
+  int m_tiles, n_tiles;
+  int whole;               // tiles in whole rounds
+  int units, cuts;         // units of the tiles left, stretches they are cut into
+  int snap;                // a cut so near to a tile's border is moved there
+  int stages, a_rows;      // rows of A8 in a stage
+  int tma_out;             // out can be written by TMA
+  uint32_t* err;
+  int32_t* tickets;        // [tiles left][CG][warps], zero between calls
+  float* parts;            // [CTAs][2] partial results: [BN / 4][128][4]
+};
+
+template <int CG_, int BN_, int DT_>
+struct MatmulCfg {
+  static constexpr int CG = CG_, BN = BN_, DT = DT_;
+  static constexpr int kEpi = 4 * (BN / 128);      // epilogue warps
+  static constexpr int kThreads = 64 + 32 * kEpi;
+  static constexpr int kBufs = 512 / BN;
+  static constexpr int kPart = 128 * BN;
+  static constexpr int kB = 128 * 128;             // bytes of W8 in a stage: 128 rows per CTA
+  static_assert(BN == 128 * CG, "each CTA of a tile loads 128 rows of W8");
+  static constexpr int kStaging = kEpi * 4096;
+  static constexpr int kMaxStages = 12;
+  static constexpr int kFixed = 1024 + kStaging + 1024;
+};
+constexpr int kSmemLimit = 232448;
+
+struct Cuts {
+  int units, cuts, snap, kb;
+  __device__ __forceinline__ int at(int c) const {  // where stretch c starts
+    if (c >= cuts) return units;
+    const int u = (int)((int64_t)units * c / cuts), in = u % kb;
+    return in <= snap ? u - in : kb - in <= snap ? u + kb - in : u;
+  }
+  __device__ __forceinline__ int owner(int u) const {
+    int c = (int)((int64_t)u * cuts / units);
+    while (c + 1 < cuts && at(c + 1) <= u) ++c;
+    while (c > 0 && at(c) > u) --c;
+    return c;
+  }
+};
+
+// The pieces of a CTA (or pair): whole tiles, then its stretch of the tiles left.
+struct Walk {
+  int tile, k0, k1;  // the piece
+  int next_whole, u, u_end, step;
+  __device__ __forceinline__ Walk(const MatmulParams& p, const Cuts& c, int id, int n) : next_whole(id), step(n) {
+    u = c.at(id);
+    u_end = c.at(id + 1);
+  }
+  __device__ __forceinline__ bool next(const MatmulParams& p) {
+    if (next_whole < p.whole) {
+      tile = next_whole;
+      next_whole += step;
+      k0 = 0;
+      k1 = p.kb;
+      return true;
+    }
+    if (u >= u_end) return false;
+    const int t = u / p.kb;
+    tile = p.whole + t;
+    k0 = u - t * p.kb;
+    k1 = min(p.kb, k0 + u_end - u);
+    u += k1 - k0;
+    return true;
+  }
+  // Tiles are ordered in bands of kBand rows of tiles, column by column: CTAs at work at the same time share rows and columns.
+  __device__ __forceinline__ void place(const MatmulParams& p, int& m, int& n) const {
+    constexpr int kBand = 8;
+    const int band = tile / (kBand * p.n_tiles), height = min(kBand, p.m_tiles - band * kBand);
+    const int in = tile - band * kBand * p.n_tiles;
+    n = in / height;
+    m = band * kBand + in - n * height;
+  }
+};
+
+// c + a * b, two at a time in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 y;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return y;
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, 1)
+    matmul8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
+                   const __grid_constant__ CUtensorMap map_o, const __grid_constant__ MatmulParams p) {
+  constexpr int CG = C::CG, BN = C::BN, DT = C::DT;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  // the MMA reads 128 rows of A8 from a stage's start, whatever the stage holds: rows past a_rows are other
+  // stages' and end in lanes that nobody reads
+  const int a_bytes = p.a_rows * 128;
+  uint8_t* staging = smem;
+  uint8_t* sa = smem + C::kStaging;
+  uint8_t* sw = sa + (size_t)p.stages * a_bytes;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sw + (size_t)p.stages * C::kB);
+  uint64_t *full = bar, *empty = full + C::kMaxStages, *acc_full = empty + C::kMaxStages, *acc_empty = acc_full + C::kBufs;
+  uint64_t* drain = acc_empty + C::kBufs;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 1 ? 0 : cluster_rank();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < C::kBufs; ++s) {
+      mbar_init(&acc_full[s], 1);
+      mbar_init(&acc_empty[s], CG * C::kEpi);
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane < 3) prefetch_map(lane == 0 ? &map_a : lane == 1 ? &map_w : &map_o);
+  if (warp == 1) tmem_alloc_cg<CG>(tmem_slot, 512);
+  tc_fence_before();
+  if constexpr (CG == 1) __syncthreads();
+  else cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   pdl_entry();
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * kTile;
-  for (int64_t t0 = (int64_t)blockIdx.y * kTile; t0 < a.T; t0 += (int64_t)gridDim.y * kTile) {
-    float acc[4][4] = {};
-    for (int k0 = 0, kb = 0; k0 < a.K; k0 += 128, ++kb) {
-      float part[4][4] = {};
-      for (int k1 = k0; k1 < min(k0 + 128, a.K); k1 += 32) {
-        __syncthreads();
-        for (int i = tid; i < kTile * 32; i += 256) {
-          const int r = i >> 5, c = i & 31;
-          const bool in = k1 + c < a.K;
-          __nv_fp8_e4m3 x, w;
-          x.__x = in && t0 + r < a.T ? a.a8[(t0 + r) * a.a8_stride + k1 + c] : 0;
-          w.__x = in && n0 + r < a.N ? a.w8[(n0 + r) * a.w8_stride + k1 + c] : 0;
-          sa[c][r] = (float)x;
-          sw[c][r] = (float)w;
+
+  const Cuts cuts{p.units, p.cuts, p.snap, p.kb};
+  const int id = (int)(blockIdx.x / CG);
+  Walk w(p, cuts, id, (int)(gridDim.x / CG));
+  bool ok = true;
+  int m, n;
+
+  if (warp == 0) {
+    if (elect_one()) {
+      uint32_t c = 0, s = 0, turn = 0;
+      while (ok && w.next(p)) {
+        w.place(p, m, n);
+        const int row = (m * CG + (int)rank) * 128, col = (n * CG + (int)rank) * 128;
+        for (int k = w.k0; k < w.k1; ++k) {
+          ok = mbar_wait_cluster(&empty[s], turn ^ 1u, p.err);
+          if (!ok) break;
+          if constexpr (CG == 1) {
+            mbar_arrive_expect_tx(&full[s], a_bytes + C::kB);
+            tma_2d(sw + s * C::kB, &map_w, k * 128, col, &full[s]);
+            tma_2d(sa + s * a_bytes, &map_a, k * 128, row, &full[s]);
+          } else {
+            // both CTAs' bytes are counted where the MMAs are issued
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (a_bytes + C::kB));
+            const uint32_t to = cluster_addr(&full[s], 0);
+            tma_2d_pair(sw + s * C::kB, &map_w, k * 128, col, to);
+            tma_2d_pair(sa + s * a_bytes, &map_a, k * 128, row, to);
+          }
+          ++c;
+          if (++s == (uint32_t)p.stages) s = 0, turn ^= 1u;
         }
-        __syncthreads();
-        for (int c = 0; c < 32; ++c)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) part[i][j] = fmaf(sa[c][ty * 4 + i], sw[c][tx + 16 * j], part[i][j]);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t t = t0 + ty * 4 + i;
-        const float as = t < a.T ? a.a_scales[t * a.a_scales_stride + (a.a_blocks > 1 ? kb : 0)] : 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t n = n0 + tx + 16 * j;
-          const float ws = n < a.N ? a.w_scales[(n >> 7) * a.w_scales_stride + kb] : 0.f;
-          acc[i][j] = fmaf(part[i][j], as * ws, acc[i][j]);
+      if (!ok) {  // copies in flight land long before this, and before shared memory goes away
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 2000000) {
         }
       }
     }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0 && elect_one()) {
+      constexpr uint32_t kId = idesc_e4m3(128 * CG, BN);
+      const uint64_t da = desc_sw128(smem_u32(sa)), dw = desc_sw128(smem_u32(sw));
+      uint32_t s = 0, turn = 0, buf = 0, buf_turn = 0;
+      while (ok && w.next(p)) {
+        for (int k = w.k0; k < w.k1; ++k) {
+          ok = mbar_wait_cluster(&acc_empty[buf], buf_turn ^ 1u, p.err) && mbar_wait_cluster(&full[s], turn, p.err);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t a = da + ((uint32_t)(s * a_bytes) >> 4), b = dw + ((uint32_t)(s * C::kB) >> 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t t = t0 + ty * 4 + i, n = n0 + tx + 16 * j;
-        if (t < a.T && n < a.N) ((uint16_t*)a.out)[t * a.out_stride + n] = from_f32<DT>(acc[i][j]);
+          for (int j = 0; j < 4; ++j) mma_f8_ss<CG>(tmem + buf * BN, a + j * 2, b + j * 2, kId, j > 0);
+          mma_commit_cg<CG>(&empty[s]);
+          mma_commit_cg<CG>(&acc_full[buf]);
+          if (++s == (uint32_t)p.stages) s = 0, turn ^= 1u;
+          if (++buf == C::kBufs) buf = 0, buf_turn ^= 1u;
+        }
       }
+      mma_commit_cg<CG>(drain);  // every MMA issued, and every arrival on the other CTA's barriers, is through
+    }
+    __syncwarp();
+    mbar_wait_cluster(drain, 0, p.err);
+  } else {
+    const int e = warp - 2, quarter = warp & 3, half = e >> 2;
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    uint8_t* stage = staging + e * 4096;
+    uint32_t buf = 0, buf_turn = 0;
+    while (ok && w.next(p)) {
+      w.place(p, m, n);
+      const int row0 = (m * CG + (int)rank) * 128 + quarter * 32, col0 = n * BN + half * 128;
+      const bool live = row0 < p.a.T && col0 < p.a.N;
+      const float* as = p.a.a_scales + (int64_t)min(row0 + lane, p.a.T - 1) * p.a.a_scales_stride;
+      const float* ws = p.a.w_scales + (int64_t)min(col0 >> 7, (p.a.N - 1) >> 7) * p.a.w_scales_stride;
+      const int a_step = p.a.a_blocks > 1 ? 1 : 0;
+      float2 acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
+      float next_a = __ldg(as + w.k0 * a_step), next_w = __ldg(ws + w.k0);
+      for (int k = w.k0; k < w.k1; ++k) {
+        const float s = next_a * next_w;
+        if (k + 1 < w.k1) next_a = __ldg(as + (k + 1) * a_step), next_w = __ldg(ws + k + 1);
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&acc_full[buf], buf_turn, p.err));
+        if (!ok) break;
+        tc_fence_after();
+        if (live) {
+          const float2 s2 = make_float2(s, s);
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(tmem + lane_base + buf * BN + half * 128 + c, v);
+            tmem_wait_ld32(v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              acc[c / 2 + i] = fma2(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s2, acc[c / 2 + i]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 1) mbar_arrive(&acc_empty[buf]);
+          else mbar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
+        }
+        if (++buf == C::kBufs) buf = 0, buf_turn ^= 1u;
+      }
+      if (!ok) break;
+      if (!live) continue;
+      if (w.k1 - w.k0 < p.kb) {  // a piece: the tile's last adds them all
+        const int t = w.tile - p.whole, first = cuts.owner(t * p.kb), pieces = cuts.owner((t + 1) * p.kb - 1) - first + 1;
+        const auto part_of = [&](int c) {  // a stretch's piece at a tile's start, and its other one
+          return reinterpret_cast<float4*>(p.parts + ((int64_t)(c * CG + (int)rank) * 2 + (c == first ? 1 : 0)) * C::kPart) +
+                 half * 32 * 128 + quarter * 32 + lane;
+        };
+        float4* mine = part_of(id);
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          mine[c * 128] = make_float4(acc[2 * c].x, acc[2 * c].y, acc[2 * c + 1].x, acc[2 * c + 1].y);
+        __threadfence();
+        __syncwarp();
+        int32_t* ticket = p.tickets + (t * CG + (int)rank) * C::kEpi + e;
+        int done = 0;
+        if (lane == 0) done = atomicAdd(ticket, 1);
+        if (__shfl_sync(0xFFFFFFFFu, done, 0) != pieces - 1) continue;
+        __threadfence();
+        if (lane == 0) *ticket = 0;
+#pragma unroll
+        for (int c = 0; c < 32; c += 8) {
+          float4 sum[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int x = first; x < first + pieces; ++x) {
+            const float4* part = part_of(x);
+            float4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __ldcg(part + (c + i) * 128);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              sum[i].x += v[i].x;
+              sum[i].y += v[i].y;
+              sum[i].z += v[i].z;
+              sum[i].w += v[i].w;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            acc[2 * (c + i)] = make_float2(sum[i].x, sum[i].y);
+            acc[2 * (c + i) + 1] = make_float2(sum[i].z, sum[i].w);
+          }
+        }
+      }
+      // 64 columns at a time through shared memory: a row of 128 bytes per lane, 16-byte pieces swizzled by row
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int col = col0 + h * 64;
+        if (col >= p.a.N) break;
+        if (lane == 0) bulk_wait_read();
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2* f = acc + h * 32 + j * 4;
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+              make_uint4(pack2<DT>(f[0].x, f[0].y), pack2<DT>(f[1].x, f[1].y), pack2<DT>(f[2].x, f[2].y), pack2<DT>(f[3].x, f[3].y));
+        }
+        if (p.tma_out) {
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&map_o, stage, col, row0);
+            bulk_commit();
+          }
+        } else {
+          __syncwarp();
+          uint16_t* out = (uint16_t*)p.a.out + (int64_t)row0 * p.a.out_stride + col;
+          const int rows = min(32, p.a.T - row0), cols = min(64, p.a.N - col);
+          for (int r = 0; r < rows; ++r, out += p.a.out_stride)
+#pragma unroll
+            for (int x = 0; x < 64; x += 32) {
+              const int at = x + lane;
+              if (at < cols) out[at] = *reinterpret_cast<const uint16_t*>(stage + r * 128 + (((at >> 3) ^ (r & 7)) << 4) + (at & 7) * 2);
+            }
+        }
+      }
+    }
+    if (lane == 0) bulk_wait();
+    __syncwarp();
   }
+  tc_fence_before();
+  if constexpr (CG == 1) __syncthreads();
+  else cluster_sync();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc_cg<CG>(tmem, 512);
+  }
+}
+
+// A matrix [rows][width] of 1- or 2-byte elements in boxes of box_rows x 128 bytes with 128-byte swizzle.
+bool make_map2(CUtensorMap* map, const void* base, CUtensorMapDataType type, int size, int64_t rows, int64_t width,
+               int64_t stride, int box_rows) {
+  const TensorMapFn encode = tensor_map_fn();
+  if (!encode) return false;
+  const cuuint64_t d[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+  // the stride of a single row is never used; TMA still wants a valid one
+  const cuuint64_t s[1] = {(cuuint64_t)(rows == 1 ? (width * size + 15) / 16 * 16 : stride * size)};
+  const cuuint32_t b[2] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows}, e[2] = {1, 1};
+  return encode(map, type, 2, const_cast<void*>(base), d, s, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class C>
+bool matmul8_configure() {
+  return cudaFuncSetAttribute(matmul8_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) == cudaSuccess;
+}
+
+template <class C>
+int matmul8_launch(const moe_matmul8_ctx* ctx, const moe_matmul8_args& a, cudaStream_t stream) {
+  MatmulParams p;
+  p.a = a;
+  p.kb = (a.K + 127) / 128;
+  const int64_t m_tiles = ((int64_t)a.T + 128 * C::CG - 1) / (128 * C::CG), n_tiles = ((int64_t)a.N + C::BN - 1) / C::BN;
+  const int64_t tiles = m_tiles * n_tiles;
+  if (tiles * p.kb >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+  p.m_tiles = (int)m_tiles;
+  p.n_tiles = (int)n_tiles;
+  const int most = ctx->sm_count / C::CG;  // CTAs or pairs
+  const int left = (int)(tiles % most);
+  p.whole = (int)tiles - left;
+  p.units = left * p.kb;
+  p.cuts = std::max(left ? 1 : 0, std::min(most, p.units / kMinUnits));
+  p.snap = p.cuts ? p.units / p.cuts / 8 : 0;
+  p.a_rows = (int)std::min<int64_t>(128, (a.T + 7) / 8 * 8);
+  p.stages = std::min(C::kMaxStages, (kSmemLimit - C::kFixed) / (p.a_rows * 128 + C::kB));
+  p.tma_out = is_aligned(a.out, 16) && (a.T == 1 || a.out_stride % 8 == 0);
+  p.err = ctx->err;
+  p.tickets = ctx->tickets;
+  p.parts = ctx->parts;
+  CUtensorMap ma, mw, mo = {};
+  if (!make_map2(&ma, a.a8, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.T, a.K, a.a8_stride, p.a_rows) ||
+      !make_map2(&mw, a.w8, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.N, a.K, a.w8_stride, 128) ||
+      (p.tma_out && !make_map2(&mo, a.out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.T, a.N, a.out_stride, 32)))
+    return MOE_ERR_CUDA;
+  const int ctas = (p.whole ? most : p.cuts) * C::CG;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = C::CG;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kFixed + (size_t)p.stages * (p.a_rows * 128 + C::kB);
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = C::CG > 1 ? 2 : 1;
+  void* args[] = {&ma, &mw, &mo, &p};
+  return cudaLaunchKernelExC(&cfg, (const void*)matmul8_kernel<C>, args) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <int DT>
+using StreamMatmul = MatmulCfg<1, 128, DT>;
+template <int DT>
+using PairMatmul = MatmulCfg<2, 256, DT>;
+
+template <int DT>
+int matmul8_by_rows(const moe_matmul8_ctx* ctx, const moe_matmul8_args& a, cudaStream_t s) {
+  return a.T <= 128 ? matmul8_launch<StreamMatmul<DT>>(ctx, a, s) : matmul8_launch<PairMatmul<DT>>(ctx, a, s);
 }
 
 // Bytes a strided [rows][width] tensor spans.
@@ -115,8 +478,9 @@ Span span2(const void* p, int64_t rows, int64_t stride, int64_t width, int size)
   return {b, b + size * ((rows - 1) * stride + width)};
 }
 
-bool clear_error(const moe_matmul8_ctx* c) {
-  return cudaMemset(c->mem, 0, 256) == cudaSuccess && cudaStreamSynchronize(cudaStreamLegacy) == cudaSuccess;
+// Clears the error word and the tickets, and waits for it (streams need not wait for the default one).
+bool clear_head(const moe_matmul8_ctx* c) {
+  return cudaMemset(c->mem, 0, c->head_bytes) == cudaSuccess && cudaStreamSynchronize(cudaStreamLegacy) == cudaSuccess;
 }
 
 int matmul8_check(const moe_matmul8_args* a) {
@@ -182,14 +546,19 @@ int moe_matmul8_create(int device, moe_matmul8_ctx** out) {
   if (!c) return MOE_ERR_OOM;
   c->device = device;
   c->sm_count = prop.multiProcessorCount;
-  c->bytes = 256;
+  // error word | tickets (of each tile left over, its CTAs' epilogue warps) | partial results (two per CTA)
+  c->head_bytes = (256 + (size_t)c->sm_count * PairMatmul<0>::kEpi * 4 + 255) / 256 * 256;
+  c->bytes = c->head_bytes + 2 * (size_t)c->sm_count * sizeof(float) * PairMatmul<0>::kPart;
   if (cudaMalloc(&c->mem, c->bytes) != cudaSuccess) {
     cudaGetLastError();
     delete c;
     return MOE_ERR_OOM;
   }
   c->err = (uint32_t*)c->mem;
-  if (!clear_error(c)) {
+  c->tickets = (int32_t*)((char*)c->mem + 256);
+  c->parts = (float*)((char*)c->mem + c->head_bytes);
+  if (!clear_head(c) || !matmul8_configure<StreamMatmul<MOE_DT_BF16>>() || !matmul8_configure<StreamMatmul<MOE_DT_F16>>() ||
+      !matmul8_configure<PairMatmul<MOE_DT_BF16>>() || !matmul8_configure<PairMatmul<MOE_DT_F16>>()) {
     cudaGetLastError();
     cudaFree(c->mem);
     delete c;
@@ -204,12 +573,8 @@ int moe_matmul8_forward(moe_matmul8_ctx* ctx, void* stream, const moe_matmul8_ar
   const int st = matmul8_check(a);
   if (st != MOE_OK || a->T == 0 || a->N == 0) return st;
   DeviceGuard g(ctx->device);
-  OpsPdl pdl;
-  const dim3 grid((unsigned)((a->N + kTile - 1) / kTile), (unsigned)std::min((a->T + kTile - 1) / kTile, 65535));
-  const cudaError_t e = a->dtype == MOE_DT_BF16
-                            ? launch_pdl(matmul8_kernel<MOE_DT_BF16>, grid, dim3(256), 0, (cudaStream_t)stream, *a)
-                            : launch_pdl(matmul8_kernel<MOE_DT_F16>, grid, dim3(256), 0, (cudaStream_t)stream, *a);
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return a->dtype == MOE_DT_BF16 ? matmul8_by_rows<MOE_DT_BF16>(ctx, *a, (cudaStream_t)stream)
+                                 : matmul8_by_rows<MOE_DT_F16>(ctx, *a, (cudaStream_t)stream);
 }
 
 int moe_matmul8_get_error(moe_matmul8_ctx* ctx, uint32_t* bits) {
@@ -218,7 +583,7 @@ int moe_matmul8_get_error(moe_matmul8_ctx* ctx, uint32_t* bits) {
   uint32_t v = 0;
   if (cudaDeviceSynchronize() != cudaSuccess) return MOE_ERR_CUDA;
   if (cudaMemcpy(&v, ctx->err, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
-  if (v && !clear_error(ctx)) return MOE_ERR_CUDA;
+  if (v && !clear_head(ctx)) return MOE_ERR_CUDA;
   if (bits) *bits = v;
   return v ? MOE_ERR_DEVICE_FLAG : MOE_OK;
 }

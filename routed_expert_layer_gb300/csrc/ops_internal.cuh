@@ -2,6 +2,8 @@
 // host-side checks, launches.
 #pragma once
 
+#include <cuda.h>
+
 #include <cmath>
 #include <new>
 
@@ -96,6 +98,22 @@ inline int shift_of(int p) {
   int s = 0;
   while ((1 << s) < p) ++s;
   return s;
+}
+
+// The driver's tensor-map encoder (host-only, so it may run during stream capture), or null.
+typedef CUresult (*TensorMapFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+inline TensorMapFn tensor_map_fn() {
+  static const TensorMapFn encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      fn = nullptr;
+    return reinterpret_cast<TensorMapFn>(fn);
+  }();
+  return encode;
 }
 
 // Words of an output or input of a call, for finding outputs that share memory with another tensor of it.
