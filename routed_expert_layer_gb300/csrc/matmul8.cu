@@ -70,12 +70,15 @@ __global__ void __launch_bounds__(256) quantize_kernel(const moe_quantize8_args 
 // pieces of a tile go through the workspace and the warp that finishes last adds them in K's order (so results
 // do not depend on which one that was), for its own 32 rows and 128 columns: no warp waits for another.
 //
-// Warps. 0: TMA (a box of A8 and one of W8 per unit). 1: issues the MMAs (of a pair: the first CTA's). 2..: epilogue, a
-// thread per row, 128 columns each.
+// Warps. 0: TMA (a box of A8 and one of W8 per unit). 1: issues the MMAs (of a pair: the first CTA's). 2: brings the scales
+// of 8 units at a time to shared memory (rows of scales are read along K, the epilogue wants them down the rows). 4..:
+// epilogue, a thread per row, 128 columns each.
 
 using namespace ptx;
 
-constexpr int kMinUnits = 4;  // units of a stretch at least
+constexpr int kMinUnits = 4;    // units of a stretch at least
+constexpr int kChunk = 8;       // units whose scales are fetched at a time
+constexpr int kScaleRow = 132;  // a unit's row scales in shared memory: 128, and 4 so that lanes on 8 units meet in no bank
 
 struct MatmulParams {
   moe_matmul8_args a;
@@ -95,14 +98,18 @@ template <int CG_, int BN_, int DT_>
 struct MatmulCfg {
   static constexpr int CG = CG_, BN = BN_, DT = DT_;
   static constexpr int kEpi = 4 * (BN / 128);      // epilogue warps
-  static constexpr int kThreads = 64 + 32 * kEpi;
+  static constexpr int kThreads = 128 + 32 * kEpi;
   static constexpr int kBufs = 512 / BN;
   static constexpr int kPart = 128 * BN;
   static constexpr int kB = 128 * 128;             // bytes of W8 in a stage: 128 rows per CTA
   static_assert(BN == 128 * CG, "each CTA of a tile loads 128 rows of W8");
   static constexpr int kStaging = kEpi * 4096;
   static constexpr int kMaxStages = 12;
-  static constexpr int kFixed = 1024 + kStaging + 1024;
+  static constexpr int kScales = kChunk * (kScaleRow + BN / 128);  // floats of a chunk's scales
+  static constexpr int kFixed = 1024 + kStaging + 2 * kScales * 4 + 512;
+  // Registers of the first warpgroup and of the epilogue's, where launching with an equal share gives the latter too few:
+  // 384 threads of 168 are 128 of 56 and 256 of 224.
+  static constexpr bool kMoveRegs = kThreads > 256;
 };
 constexpr int kSmemLimit = 232448;
 
@@ -180,8 +187,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   uint8_t* sw = sa + (size_t)p.stages * a_bytes;
   uint64_t* bar = reinterpret_cast<uint64_t*>(sw + (size_t)p.stages * C::kB);
   uint64_t *full = bar, *empty = full + C::kMaxStages, *acc_full = empty + C::kMaxStages, *acc_empty = acc_full + C::kBufs;
-  uint64_t* drain = acc_empty + C::kBufs;
+  uint64_t *scale_full = acc_empty + C::kBufs, *scale_empty = scale_full + 2, *drain = scale_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  float* scales = reinterpret_cast<float*>(bar + 64);  // [2][kChunk][kScaleRow | BN / 128]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 1 ? 0 : cluster_rank();
@@ -193,6 +201,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     for (int s = 0; s < C::kBufs; ++s) {
       mbar_init(&acc_full[s], 1);
       mbar_init(&acc_empty[s], CG * C::kEpi);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&scale_full[s], 1);
+      mbar_init(&scale_empty[s], C::kEpi);
     }
     mbar_init(drain, 1);
     fence_mbar_init();
@@ -212,99 +224,55 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   bool ok = true;
   int m, n;
 
-  if (warp == 0) {
-    if (elect_one()) {
-      uint32_t c = 0, s = 0, turn = 0;
-      while (ok && w.next(p)) {
-        w.place(p, m, n);
-        const int row = (m * CG + (int)rank) * 128, col = (n * CG + (int)rank) * 128;
-        for (int k = w.k0; k < w.k1; ++k) {
-          ok = mbar_wait_cluster(&empty[s], turn ^ 1u, p.err);
-          if (!ok) break;
-          if constexpr (CG == 1) {
-            mbar_arrive_expect_tx(&full[s], a_bytes + C::kB);
-            tma_2d(sw + s * C::kB, &map_w, k * 128, col, &full[s]);
-            tma_2d(sa + s * a_bytes, &map_a, k * 128, row, &full[s]);
-          } else {
-            // both CTAs' bytes are counted where the MMAs are issued
-            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (a_bytes + C::kB));
-            const uint32_t to = cluster_addr(&full[s], 0);
-            tma_2d_pair(sw + s * C::kB, &map_w, k * 128, col, to);
-            tma_2d_pair(sa + s * a_bytes, &map_a, k * 128, row, to);
-          }
-          ++c;
-          if (++s == (uint32_t)p.stages) s = 0, turn ^= 1u;
-        }
-      }
-      if (!ok) {  // copies in flight land long before this, and before shared memory goes away
-        const uint64_t t0 = globaltimer();
-        while (globaltimer() - t0 < 2000000) {
-        }
-      }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (rank == 0 && elect_one()) {
-      constexpr uint32_t kId = idesc_e4m3(128 * CG, BN);
-      const uint64_t da = desc_sw128(smem_u32(sa)), dw = desc_sw128(smem_u32(sw));
-      uint32_t s = 0, turn = 0, buf = 0, buf_turn = 0;
-      while (ok && w.next(p)) {
-        for (int k = w.k0; k < w.k1; ++k) {
-          ok = mbar_wait_cluster(&acc_empty[buf], buf_turn ^ 1u, p.err) && mbar_wait_cluster(&full[s], turn, p.err);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t a = da + ((uint32_t)(s * a_bytes) >> 4), b = dw + ((uint32_t)(s * C::kB) >> 4);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) mma_f8_ss<CG>(tmem + buf * BN, a + j * 2, b + j * 2, kId, j > 0);
-          mma_commit_cg<CG>(&empty[s]);
-          mma_commit_cg<CG>(&acc_full[buf]);
-          if (++s == (uint32_t)p.stages) s = 0, turn ^= 1u;
-          if (++buf == C::kBufs) buf = 0, buf_turn ^= 1u;
-        }
-      }
-      mma_commit_cg<CG>(drain);  // every MMA issued, and every arrival on the other CTA's barriers, is through
-    }
-    __syncwarp();
-    mbar_wait_cluster(drain, 0, p.err);
-  } else {
-    const int e = warp - 2, quarter = warp & 3, half = e >> 2;
+  if (warp >= 4) {
+    if constexpr (C::kMoveRegs) regs_up<224>();
+    const int e = warp - 4, quarter = warp & 3, half = e >> 2;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     uint8_t* stage = staging + e * 4096;
-    uint32_t buf = 0, buf_turn = 0;
+    uint32_t buf = 0, buf_turn = 0, sbuf = 0, sturn = 0;
     while (ok && w.next(p)) {
       w.place(p, m, n);
       const int row0 = (m * CG + (int)rank) * 128 + quarter * 32, col0 = n * BN + half * 128;
       const bool live = row0 < p.a.T && col0 < p.a.N;
-      const float* as = p.a.a_scales + (int64_t)min(row0 + lane, p.a.T - 1) * p.a.a_scales_stride;
-      const float* ws = p.a.w_scales + (int64_t)min(col0 >> 7, (p.a.N - 1) >> 7) * p.a.w_scales_stride;
-      const int a_step = p.a.a_blocks > 1 ? 1 : 0;
       float2 acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
-      float next_a = __ldg(as + w.k0 * a_step), next_w = __ldg(ws + w.k0);
       for (int k = w.k0; k < w.k1; ++k) {
-        const float s = next_a * next_w;
-        if (k + 1 < w.k1) next_a = __ldg(as + (k + 1) * a_step), next_w = __ldg(ws + k + 1);
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&acc_full[buf], buf_turn, p.err));
+        const int x = (k - w.k0) & (kChunk - 1);
+        if (x == 0) ok = mbar_wait_suspended(&scale_full[sbuf], sturn, p.err);
+        const float* sc = scales + sbuf * C::kScales;
+        const float s = sc[x * kScaleRow + quarter * 32 + lane] * sc[kChunk * kScaleRow + x * (BN / 128) + half];
+        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait_suspended(&acc_full[buf], buf_turn, p.err));
         if (!ok) break;
         tc_fence_after();
+        const auto release = [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (CG == 1) mbar_arrive(&acc_empty[buf]);
+            else mbar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
+          }
+        };
         if (live) {
+          const uint32_t from = tmem + lane_base + buf * BN + half * 128;
           const float2 s2 = make_float2(s, s);
+          uint32_t v[2][32];
+          tmem_ld32(from, v[0]);
 #pragma unroll
-          for (int c = 0; c < 128; c += 32) {
-            uint32_t v[32];
-            tmem_ld32(tmem + lane_base + buf * BN + half * 128 + c, v);
-            tmem_wait_ld32(v);
+          for (int c = 0; c < 4; ++c) {
+            tmem_wait_ld32(v[c & 1]);
+            if (c < 3) tmem_ld32(from + (c + 1) * 32, v[(c + 1) & 1]);
+            else release();
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              acc[c / 2 + i] = fma2(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s2, acc[c / 2 + i]);
+              acc[c * 16 + i] = fma2(make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), s2, acc[c * 16 + i]);
           }
+        } else {
+          release();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (CG == 1) mbar_arrive(&acc_empty[buf]);
-          else mbar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
+        if (x == kChunk - 1 || k + 1 == w.k1) {
+          if (lane == 0) mbar_arrive(&scale_empty[sbuf]);
+          if (++sbuf == 2) sbuf = 0, sturn ^= 1u;
         }
         if (++buf == C::kBufs) buf = 0, buf_turn ^= 1u;
       }
@@ -329,27 +297,21 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         __threadfence();
         if (lane == 0) *ticket = 0;
 #pragma unroll
-        for (int c = 0; c < 32; c += 8) {
-          float4 sum[8];
+        for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
+        for (int x = first; x < first + pieces; ++x) {
+          const float4* part = part_of(x);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int x = first; x < first + pieces; ++x) {
-            const float4* part = part_of(x);
-            float4 v[8];
+          for (int c = 0; c < 32; c += 16) {
+            float4 v[16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __ldcg(part + (c + i) * 128);
+            for (int i = 0; i < 16; ++i) v[i] = __ldcg(part + (c + i) * 128);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              sum[i].x += v[i].x;
-              sum[i].y += v[i].y;
-              sum[i].z += v[i].z;
-              sum[i].w += v[i].w;
+            for (int i = 0; i < 16; ++i) {
+              acc[2 * (c + i)].x += v[i].x;
+              acc[2 * (c + i)].y += v[i].y;
+              acc[2 * (c + i) + 1].x += v[i].z;
+              acc[2 * (c + i) + 1].y += v[i].w;
             }
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            acc[2 * (c + i)] = make_float2(sum[i].x, sum[i].y);
-            acc[2 * (c + i) + 1] = make_float2(sum[i].z, sum[i].w);
           }
         }
       }
@@ -388,6 +350,88 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     }
     if (lane == 0) bulk_wait();
     __syncwarp();
+  } else {
+    if constexpr (C::kMoveRegs) regs_down<56>();
+    if (warp == 0) {
+      if (elect_one()) {
+        uint32_t s = 0, turn = 0;
+        while (ok && w.next(p)) {
+          w.place(p, m, n);
+          const int row = (m * CG + (int)rank) * 128, col = (n * CG + (int)rank) * 128;
+          for (int k = w.k0; k < w.k1; ++k) {
+            ok = mbar_wait_suspended(&empty[s], turn ^ 1u, p.err);
+            if (!ok) break;
+            if constexpr (CG == 1) {
+              mbar_arrive_expect_tx(&full[s], a_bytes + C::kB);
+              tma_2d(sw + s * C::kB, &map_w, k * 128, col, &full[s]);
+              tma_2d(sa + s * a_bytes, &map_a, k * 128, row, &full[s]);
+            } else {
+              // both CTAs' bytes are counted where the MMAs are issued
+              if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (a_bytes + C::kB));
+              const uint32_t to = cluster_addr(&full[s], 0);
+              tma_2d_pair(sw + s * C::kB, &map_w, k * 128, col, to);
+              tma_2d_pair(sa + s * a_bytes, &map_a, k * 128, row, to);
+            }
+            if (++s == (uint32_t)p.stages) s = 0, turn ^= 1u;
+          }
+        }
+        if (!ok) {  // copies in flight land long before this, and before shared memory goes away
+          const uint64_t t0 = globaltimer();
+          while (globaltimer() - t0 < 2000000) {
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      if (rank == 0 && elect_one()) {
+        constexpr uint32_t kId = idesc_e4m3(128 * CG, BN);
+        const uint64_t da = desc_sw128(smem_u32(sa)), dw = desc_sw128(smem_u32(sw));
+        uint32_t s = 0, turn = 0, buf = 0, buf_turn = 0;
+        while (ok && w.next(p)) {
+          for (int k = w.k0; k < w.k1; ++k) {
+            ok = mbar_wait_suspended(&acc_empty[buf], buf_turn ^ 1u, p.err) && mbar_wait_suspended(&full[s], turn, p.err);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t a = da + ((uint32_t)(s * a_bytes) >> 4), b = dw + ((uint32_t)(s * C::kB) >> 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mma_f8_ss<CG>(tmem + buf * BN, a + j * 2, b + j * 2, kId, j > 0);
+            mma_commit_cg<CG>(&empty[s]);
+            mma_commit_cg<CG>(&acc_full[buf]);
+            if (++s == (uint32_t)p.stages) s = 0, turn ^= 1u;
+            if (++buf == C::kBufs) buf = 0, buf_turn ^= 1u;
+          }
+        }
+        mma_commit_cg<CG>(drain);  // every MMA issued, and every arrival on the other CTA's barriers, is through
+      }
+      __syncwarp();
+      mbar_wait_suspended(drain, 0, p.err);
+    } else if (warp == 2) {
+      uint32_t buf = 0, turn = 0;
+      const int x = lane & (kChunk - 1), y = lane / kChunk;  // unit and row of a lane
+      constexpr int kRows = 32 / kChunk;
+      while (ok && w.next(p)) {
+        w.place(p, m, n);
+        const int row0 = (m * CG + (int)rank) * 128, rows = min(128, p.a.T - row0), block0 = n * (BN / 128);
+        for (int k = w.k0; k < w.k1; k += kChunk) {
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_suspended(&scale_empty[buf], turn ^ 1u, p.err));
+          if (!ok) break;
+          float* to = scales + buf * C::kScales + x * kScaleRow;
+          const bool in = k + x < w.k1;
+          const float* from = p.a.a_scales + (int64_t)row0 * p.a.a_scales_stride + (p.a.a_blocks > 1 ? k + x : 0);
+#pragma unroll 16
+          for (int r = y; r < 128; r += kRows) {
+            const float v = in && r < rows ? __ldg(from + r * p.a.a_scales_stride) : 0.f;
+            to[r] = v;
+          }
+          if (y < BN / 128)
+            scales[buf * C::kScales + kChunk * kScaleRow + x * (BN / 128) + y] =
+                in && block0 + y <= (p.a.N - 1) >> 7 ? __ldg(p.a.w_scales + (block0 + y) * p.a.w_scales_stride + k + x) : 0.f;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&scale_full[buf]);
+          if (++buf == 2) buf = 0, turn ^= 1u;
+        }
+      }
+    }
   }
   tc_fence_before();
   if constexpr (CG == 1) __syncthreads();
