@@ -276,7 +276,7 @@ MOE_API int moe_quantize8(void* stream, const moe_quantize8_args* a);
  * scale per row. The scales are as moe_add_rmsnorm (group 0, 128) and moe_quantize8 write them;
  * rows of every tensor may be strided. K a multiple of 16, a8 and w8 16-byte aligned with row strides that
  * are multiples of 16; out is aligned to its elements and shares no byte with an input.
- * T, N >= 0; T or N 0: nothing is done. K >= 16. */
+ * T, N >= 0; T or N 0: nothing is done. 16 <= K <= 2^20. */
 typedef struct {
   const uint8_t* a8;
   const float* a_scales;

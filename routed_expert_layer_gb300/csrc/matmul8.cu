@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const moe_quantize8_args 
 // pieces of a tile go through the workspace and the warp that finishes last adds them in K's order (so results
 // do not depend on which one that was), for its own 32 rows and 128 columns: no warp waits for another.
 //
-// Warps. 0: TMA (a box of A8 and one of W8 per unit). 1: issues the MMAs (of a pair: the first CTA's). 2: brings the scales
+// Warps. 0: TMA (a stage: a unit's rows of A8 and W8). 1: issues the MMAs (of a pair: the first CTA's). 2, 3: bring the scales
 // of 8 units at a time to shared memory (rows of scales are read along K, the epilogue wants them down the rows). 4..:
 // epilogue, a thread per row, 128 columns each.
 
@@ -91,7 +91,7 @@ struct MatmulParams {
   int tma_out;             // out can be written by TMA
   uint32_t* err;
   int32_t* tickets;        // [tiles left][CG][warps], zero between calls
-  float* parts;            // [CTAs][2] partial results: [BN / 4][128][4]
+  float* parts;            // [CTAs][2] partial results: [warps][128 columns / 4][32 rows][4]
 };
 
 template <int CG_, int BN_, int DT_>
@@ -99,16 +99,18 @@ struct MatmulCfg {
   static constexpr int CG = CG_, BN = BN_, DT = DT_;
   static constexpr int kEpi = 4 * (BN / 128);      // epilogue warps
   static constexpr int kThreads = 128 + 32 * kEpi;
-  static constexpr int kBufs = 512 / BN;
+  static constexpr int kBlocks = BN / 128;         // blocks of W8's scales in a tile
+  static constexpr int kBufs = 4;                  // products of 128 columns in tensor memory
+  static constexpr int kDeep = kBufs / kBlocks;    // of units
   static constexpr int kPart = 128 * BN;
   static constexpr int kB = 128 * 128;             // bytes of W8 in a stage: 128 rows per CTA
   static_assert(BN == 128 * CG, "each CTA of a tile loads 128 rows of W8");
   static constexpr int kStaging = kEpi * 4096;
   static constexpr int kMaxStages = 12;
   static constexpr int kScales = kChunk * (kScaleRow + BN / 128);  // floats of a chunk's scales
-  static constexpr int kFixed = 1024 + kStaging + 2 * kScales * 4 + 512;
+  static constexpr int kFixed = 1024 + kStaging + 2 * kScales * 4 + 32 * kEpi + 512;
   // Registers of the first warpgroup and of the epilogue's, where launching with an equal share gives the latter too few:
-  // 384 threads of 168 are 128 of 56 and 256 of 224.
+  // 384 threads of 168 are 128 of 72 and 256 of 216.
   static constexpr bool kMoveRegs = kThreads > 256;
 };
 constexpr int kSmemLimit = 232448;
@@ -117,11 +119,11 @@ struct Cuts {
   int units, cuts, snap, kb;
   __device__ __forceinline__ int at(int c) const {  // where stretch c starts
     if (c >= cuts) return units;
-    const int u = (int)((int64_t)units * c / cuts), in = u % kb;
+    const int u = units * c / cuts, in = u % kb;  // (below 2^31: K <= 2^20)
     return in <= snap ? u - in : kb - in <= snap ? u + kb - in : u;
   }
   __device__ __forceinline__ int owner(int u) const {
-    int c = (int)((int64_t)u * cuts / units);
+    int c = u * cuts / units;
     while (c + 1 < cuts && at(c + 1) <= u) ++c;
     while (c > 0 && at(c) > u) --c;
     return c;
@@ -162,6 +164,18 @@ struct Walk {
   }
 };
 
+// mbar_wait by a whole warp, with one answer for all its lanes. (Its first look costs 15 cycles; mbar_wait_suspended's takes
+// 94 for a barrier that is ready, and a unit's 512 cycles of products see several waits in a row.)
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint32_t* err) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, err));
+}
+
+__device__ __forceinline__ int load_acquire(const int32_t* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // c + a * b, two at a time in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 y;
@@ -200,10 +214,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     }
     for (int s = 0; s < C::kBufs; ++s) {
       mbar_init(&acc_full[s], 1);
-      mbar_init(&acc_empty[s], CG * C::kEpi);
+      mbar_init(&acc_empty[s], CG * 4);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&scale_full[s], 1);
+      mbar_init(&scale_full[s], 2);
       mbar_init(&scale_empty[s], C::kEpi);
     }
     mbar_init(drain, 1);
@@ -225,95 +239,117 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   int m, n;
 
   if (warp >= 4) {
-    if constexpr (C::kMoveRegs) regs_up<224>();
-    const int e = warp - 4, quarter = warp & 3, half = e >> 2;
+    if constexpr (C::kMoveRegs) regs_up<216>();
+    const int e = warp - 4, quarter = warp & 3, part = e >> 2;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     uint8_t* stage = staging + e * 4096;
-    uint32_t buf = 0, buf_turn = 0, sbuf = 0, sturn = 0;
+    uint32_t units = 0, chunks = 0;  // passed so far: their buffers and parities
+    const uint32_t first_empty = CG == 1 ? 0 : cluster_addr(acc_empty, 0);
+    const auto free_acc = [&](uint32_t at) {
+      if constexpr (CG == 1) mbar_arrive(&acc_empty[at]);
+      else mbar_arrive_cluster(first_empty + at * 8);
+    };
+    // the place on the work is out of the registers while units are added up
+    Walk* const parked = reinterpret_cast<Walk*>(reinterpret_cast<uint8_t*>(scales + 2 * C::kScales) + e * 32);
+    static_assert(sizeof(Walk) <= 32, "space of a parked place");
     while (ok && w.next(p)) {
       w.place(p, m, n);
-      const int row0 = (m * CG + (int)rank) * 128 + quarter * 32, col0 = n * BN + half * 128;
-      const bool live = row0 < p.a.T && col0 < p.a.N;
+      const bool live = (m * CG + (int)rank) * 128 + quarter * 32 < p.a.T;
+      const int count = w.k1 - w.k0;
+      if (lane == 0) *parked = w;
       float2 acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
-      for (int k = w.k0; k < w.k1; ++k) {
-        const int x = (k - w.k0) & (kChunk - 1);
-        if (x == 0) ok = mbar_wait_suspended(&scale_full[sbuf], sturn, p.err);
-        const float* sc = scales + sbuf * C::kScales;
-        const float s = sc[x * kScaleRow + quarter * 32 + lane] * sc[kChunk * kScaleRow + x * (BN / 128) + half];
-        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait_suspended(&acc_full[buf], buf_turn, p.err));
+#pragma unroll 1
+      for (int k = 0; k < count; ++k, ++units) {
+        const int x = k & (kChunk - 1), buf = units % C::kDeep * C::kBlocks + part;
+        if (x == 0) ok = wait_warp(&scale_full[chunks & 1], chunks >> 1 & 1, p.err);
+        const float* sc = scales + (chunks & 1) * C::kScales;
+        const float s = sc[x * kScaleRow + quarter * 32 + lane] * sc[kChunk * kScaleRow + x * C::kBlocks + part];
+        ok = ok && wait_warp(&acc_full[buf], units / C::kDeep & 1, p.err);
         if (!ok) break;
         tc_fence_after();
-        const auto release = [&] {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (CG == 1) mbar_arrive(&acc_empty[buf]);
-            else mbar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
-          }
-        };
         if (live) {
-          const uint32_t from = tmem + lane_base + buf * BN + half * 128;
+          const uint32_t from = tmem + lane_base + buf * 128;
           const float2 s2 = make_float2(s, s);
-          uint32_t v[2][32];
+          uint32_t v[2][32];  // a load runs under the arithmetic of the one before
           tmem_ld32(from, v[0]);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             tmem_wait_ld32(v[c & 1]);
-            if (c < 3) tmem_ld32(from + (c + 1) * 32, v[(c + 1) & 1]);
-            else release();
+            if (c < 3) {
+              tmem_ld32(from + (c + 1) * 32, v[(c + 1) & 1]);
+            } else {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) free_acc(buf);
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               acc[c * 16 + i] = fma2(make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), s2, acc[c * 16 + i]);
           }
         } else {
-          release();
+          __syncwarp();
+          if (lane == 0) free_acc(buf);
         }
-        if (x == kChunk - 1 || k + 1 == w.k1) {
-          if (lane == 0) mbar_arrive(&scale_empty[sbuf]);
-          if (++sbuf == 2) sbuf = 0, sturn ^= 1u;
+        if (x == kChunk - 1 || k + 1 == count) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&scale_empty[chunks & 1]);
+          ++chunks;
         }
-        if (++buf == C::kBufs) buf = 0, buf_turn ^= 1u;
       }
       if (!ok) break;
+      __syncwarp();
+      w = *parked;
+      __syncwarp();
       if (!live) continue;
-      if (w.k1 - w.k0 < p.kb) {  // a piece: the tile's last adds them all
-        const int t = w.tile - p.whole, first = cuts.owner(t * p.kb), pieces = cuts.owner((t + 1) * p.kb - 1) - first + 1;
-        const auto part_of = [&](int c) {  // a stretch's piece at a tile's start, and its other one
-          return reinterpret_cast<float4*>(p.parts + ((int64_t)(c * CG + (int)rank) * 2 + (c == first ? 1 : 0)) * C::kPart) +
-                 half * 32 * 128 + quarter * 32 + lane;
+      w.place(p, m, n);
+      const int row0 = (m * CG + (int)rank) * 128 + quarter * 32, col0 = n * BN + part * 128;
+      if (count < p.kb) {  // a piece: the last to finish adds the tile's pieces
+        const int first = cuts.owner((w.tile - p.whole) * p.kb), pieces = cuts.owner((w.tile - p.whole + 1) * p.kb - 1) - first + 1;
+        const int index = id - first;
+        const auto part_of = [&](int i) {  // the i-th piece: a stretch's piece at a tile's start, or its other one
+          return reinterpret_cast<float4*>(p.parts + ((int64_t)((first + i) * CG + (int)rank) * 2 + (i == 0 ? 1 : 0)) * C::kPart) +
+                 e * 1024 + lane;
         };
-        float4* mine = part_of(id);
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          mine[c * 128] = make_float4(acc[2 * c].x, acc[2 * c].y, acc[2 * c + 1].x, acc[2 * c + 1].y);
-        __threadfence();
-        __syncwarp();
-        int32_t* ticket = p.tickets + (t * CG + (int)rank) * C::kEpi + e;
-        int done = 0;
-        if (lane == 0) done = atomicAdd(ticket, 1);
-        if (__shfl_sync(0xFFFFFFFFu, done, 0) != pieces - 1) continue;
-        __threadfence();
-        if (lane == 0) *ticket = 0;
-#pragma unroll
-        for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
-        for (int x = first; x < first + pieces; ++x) {
-          const float4* part = part_of(x);
+        int32_t* ticket = p.tickets + ((w.tile - p.whole) * CG + (int)rank) * C::kEpi + e;
+        const auto add = [&](int i, bool to_sum) {
+          const float4* from = part_of(i);
 #pragma unroll
           for (int c = 0; c < 32; c += 16) {
             float4 v[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __ldcg(part + (c + i) * 128);
+            for (int j = 0; j < 16; ++j) v[j] = __ldcg(from + (c + j) * 32);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              acc[2 * (c + i)].x += v[i].x;
-              acc[2 * (c + i)].y += v[i].y;
-              acc[2 * (c + i) + 1].x += v[i].z;
-              acc[2 * (c + i) + 1].y += v[i].w;
+            for (int j = 0; j < 16; ++j) {
+              float2 &a = acc[2 * (c + j)], &b = acc[2 * (c + j) + 1];
+              a = to_sum ? make_float2(a.x + v[j].x, a.y + v[j].y) : make_float2(v[j].x, v[j].y);
+              b = to_sum ? make_float2(b.x + v[j].z, b.y + v[j].w) : make_float2(v[j].z, v[j].w);
             }
           }
+        };
+        int done = 0;
+        // Where the others are done already, this piece need not be written. (In the sum's order it has to be one of the
+        // first two, which may change places.)
+        if (lane == 0 && index < 2) done = load_acquire(ticket);
+        done = __shfl_sync(0xFFFFFFFFu, done, 0);
+        if (done == pieces - 1) {
+          for (int i = 0; i < pieces; ++i)
+            if (i != index) add(i, true);
+        } else {
+          float4* mine = part_of(index);
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            mine[c * 32] = make_float4(acc[2 * c].x, acc[2 * c].y, acc[2 * c + 1].x, acc[2 * c + 1].y);
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) done = atomicAdd(ticket, 1);
+          if (__shfl_sync(0xFFFFFFFFu, done, 0) != pieces - 1) continue;
+          __threadfence();
+          add(0, false);
+          for (int i = 1; i < pieces; ++i) add(i, true);
         }
+        if (lane == 0) *ticket = 0;
       }
       // 64 columns at a time through shared memory: a row of 128 bytes per lane, 16-byte pieces swizzled by row
 #pragma unroll
@@ -351,15 +387,15 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     if (lane == 0) bulk_wait();
     __syncwarp();
   } else {
-    if constexpr (C::kMoveRegs) regs_down<56>();
+    if constexpr (C::kMoveRegs) regs_down<72>();
     if (warp == 0) {
       if (elect_one()) {
         uint32_t s = 0, turn = 0;
         while (ok && w.next(p)) {
           w.place(p, m, n);
-          const int row = (m * CG + (int)rank) * 128, col = (n * CG + (int)rank) * 128;
+          const int row = (m * CG + (int)rank) * 128, col = n * BN + (int)rank * (128 / CG);
           for (int k = w.k0; k < w.k1; ++k) {
-            ok = mbar_wait_suspended(&empty[s], turn ^ 1u, p.err);
+            ok = mbar_wait(&empty[s], turn ^ 1u, p.err);
             if (!ok) break;
             if constexpr (CG == 1) {
               mbar_arrive_expect_tx(&full[s], a_bytes + C::kB);
@@ -370,6 +406,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (a_bytes + C::kB));
               const uint32_t to = cluster_addr(&full[s], 0);
               tma_2d_pair(sw + s * C::kB, &map_w, k * 128, col, to);
+              tma_2d_pair(sw + s * C::kB + C::kB / 2, &map_w, k * 128, col + 128, to);
               tma_2d_pair(sa + s * a_bytes, &map_a, k * 128, row, to);
             }
             if (++s == (uint32_t)p.stages) s = 0, turn ^= 1u;
@@ -384,47 +421,56 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       __syncwarp();
     } else if (warp == 1) {
       if (rank == 0 && elect_one()) {
-        constexpr uint32_t kId = idesc_e4m3(128 * CG, BN);
+        constexpr uint32_t kId = idesc_e4m3(128 * CG, 128);
         const uint64_t da = desc_sw128(smem_u32(sa)), dw = desc_sw128(smem_u32(sw));
         uint32_t s = 0, turn = 0, buf = 0, buf_turn = 0;
         while (ok && w.next(p)) {
           for (int k = w.k0; k < w.k1; ++k) {
-            ok = mbar_wait_suspended(&acc_empty[buf], buf_turn ^ 1u, p.err) && mbar_wait_suspended(&full[s], turn, p.err);
-            if (!ok) break;
-            tc_fence_after();
+            ok = mbar_wait(&full[s], turn, p.err);
             const uint64_t a = da + ((uint32_t)(s * a_bytes) >> 4), b = dw + ((uint32_t)(s * C::kB) >> 4);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mma_f8_ss<CG>(tmem + buf * BN, a + j * 2, b + j * 2, kId, j > 0);
-            mma_commit_cg<CG>(&empty[s]);
-            mma_commit_cg<CG>(&acc_full[buf]);
+            for (int h = 0; h < C::kBlocks; ++h, ++buf) {
+              ok = ok && mbar_wait(&acc_empty[buf], buf_turn ^ 1u, p.err);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int j = 0; j < 4; ++j) mma_f8_ss<CG>(tmem + buf * 128, a + j * 2, b + h * (C::kB >> 5) + j * 2, kId, j > 0);
+              if (h + 1 == C::kBlocks) mma_commit_cg<CG>(&empty[s]);
+              mma_commit_cg<CG>(&acc_full[buf]);
+            }
+            if (!ok) break;
+            if (buf == C::kBufs) buf = 0, buf_turn ^= 1u;
             if (++s == (uint32_t)p.stages) s = 0, turn ^= 1u;
-            if (++buf == C::kBufs) buf = 0, buf_turn ^= 1u;
           }
         }
         mma_commit_cg<CG>(drain);  // every MMA issued, and every arrival on the other CTA's barriers, is through
       }
       __syncwarp();
-      mbar_wait_suspended(drain, 0, p.err);
-    } else if (warp == 2) {
+      mbar_wait(drain, 0, p.err);
+    } else {
       uint32_t buf = 0, turn = 0;
       const int x = lane & (kChunk - 1), y = lane / kChunk;  // unit and row of a lane
       constexpr int kRows = 32 / kChunk;
+      const int row_first = (warp - 2) * 64 + y;  // each of the two warps takes 64 rows
       while (ok && w.next(p)) {
         w.place(p, m, n);
-        const int row0 = (m * CG + (int)rank) * 128, rows = min(128, p.a.T - row0), block0 = n * (BN / 128);
+        const int row0 = (m * CG + (int)rank) * 128, rows = min(128, p.a.T - row0), block0 = n * C::kBlocks;
         for (int k = w.k0; k < w.k1; k += kChunk) {
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait_suspended(&scale_empty[buf], turn ^ 1u, p.err));
+          ok = wait_warp(&scale_empty[buf], turn ^ 1u, p.err);
           if (!ok) break;
           float* to = scales + buf * C::kScales + x * kScaleRow;
           const bool in = k + x < w.k1;
           const float* from = p.a.a_scales + (int64_t)row0 * p.a.a_scales_stride + (p.a.a_blocks > 1 ? k + x : 0);
-#pragma unroll 16
-          for (int r = y; r < 128; r += kRows) {
-            const float v = in && r < rows ? __ldg(from + r * p.a.a_scales_stride) : 0.f;
-            to[r] = v;
+          float v[64 / kRows];
+#pragma unroll
+          for (int i = 0; i < 64 / kRows; ++i) {
+            const int r = row_first + i * kRows;
+            v[i] = in && r < rows ? __ldg(from + r * p.a.a_scales_stride) : 0.f;
           }
-          if (y < BN / 128)
-            scales[buf * C::kScales + kChunk * kScaleRow + x * (BN / 128) + y] =
+#pragma unroll
+          for (int i = 0; i < 64 / kRows; ++i) to[row_first + i * kRows] = v[i];
+          if (warp == 2 && y < C::kBlocks)
+            scales[buf * C::kScales + kChunk * kScaleRow + x * C::kBlocks + y] =
                 in && block0 + y <= (p.a.N - 1) >> 7 ? __ldg(p.a.w_scales + (block0 + y) * p.a.w_scales_stride + k + x) : 0.f;
           __syncwarp();
           if (lane == 0) mbar_arrive(&scale_full[buf]);
@@ -476,7 +522,7 @@ int matmul8_launch(const moe_matmul8_ctx* ctx, const moe_matmul8_args& a, cudaSt
   p.whole = (int)tiles - left;
   p.units = left * p.kb;
   p.cuts = std::max(left ? 1 : 0, std::min(most, p.units / kMinUnits));
-  p.snap = p.cuts ? p.units / p.cuts / 8 : 0;
+  p.snap = p.cuts ? p.units / p.cuts / 16 : 0;
   p.a_rows = (int)std::min<int64_t>(128, (a.T + 7) / 8 * 8);
   p.stages = std::min(C::kMaxStages, (kSmemLimit - C::kFixed) / (p.a_rows * 128 + C::kB));
   p.tma_out = is_aligned(a.out, 16) && (a.T == 1 || a.out_stride % 8 == 0);
@@ -485,7 +531,7 @@ int matmul8_launch(const moe_matmul8_ctx* ctx, const moe_matmul8_args& a, cudaSt
   p.parts = ctx->parts;
   CUtensorMap ma, mw, mo = {};
   if (!make_map2(&ma, a.a8, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.T, a.K, a.a8_stride, p.a_rows) ||
-      !make_map2(&mw, a.w8, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.N, a.K, a.w8_stride, 128) ||
+      !make_map2(&mw, a.w8, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.N, a.K, a.w8_stride, 128 / C::CG) ||
       (p.tma_out && !make_map2(&mo, a.out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.T, a.N, a.out_stride, 32)))
     return MOE_ERR_CUDA;
   const int ctas = (p.whole ? most : p.cuts) * C::CG;
@@ -532,6 +578,7 @@ int matmul8_check(const moe_matmul8_args* a) {
     return MOE_ERR_INVALID_ARG;
   const int blocks = (a->K + 127) / 128;
   if (a->a_blocks != blocks && a->a_blocks != 1) return MOE_ERR_INVALID_ARG;
+  if (a->K > 1 << 20) return MOE_ERR_UNSUPPORTED;
   if (a->T == 0 || a->N == 0) return MOE_OK;
   if (!a->a8 || !a->w8 || !a->a_scales || !a->w_scales || !a->out || !is_aligned(a->a8, 16) || !is_aligned(a->w8, 16) ||
       !is_aligned(a->a_scales, 4) || !is_aligned(a->w_scales, 4) || !is_aligned(a->out, 2))
