@@ -252,8 +252,8 @@ cudaError_t quantize(const moe_quantize8_args& a, cudaStream_t s) {
 
 using namespace ptx;
 
-constexpr int kMinUnits = 4;    // units of a stretch at least
 constexpr int kChunk = 8;       // units whose scales are fetched at a time
+constexpr int kParked = 48;     // bytes of an epilogue warp's parked place
 constexpr int kScaleRow = 132;  // a unit's row scales in shared memory: 128, and 4 so that lanes on 8 units meet in no bank
 
 struct MatmulParams {
@@ -283,8 +283,9 @@ struct MatmulCfg {
   static_assert(BN == 128 * CG, "each CTA of a tile loads 128 rows of W8");
   static constexpr int kStaging = kEpi * 4096;
   static constexpr int kMaxStages = 12;
+  static constexpr double kUnitUs = CG == 1 ? 0.25 : 0.5;  // a unit's time on the SM
   static constexpr int kScales = kChunk * (kScaleRow + BN / 128);  // floats of a chunk's scales
-  static constexpr int kFixed = 1024 + kStaging + 2 * kScales * 4 + 32 * kEpi + 512;
+  static constexpr int kFixed = 1024 + kStaging + 2 * kScales * 4 + kParked * kEpi + 512;
   // Registers of the first warpgroup and of the epilogue's, where launching with an equal share gives the latter too few:
   // 384 threads of 168 are 128 of 72 and 256 of 216.
   static constexpr bool kMoveRegs = kThreads > 256;
@@ -298,11 +299,13 @@ struct Cuts {
     const int u = units * c / cuts, in = u % kb;  // (below 2^31: K <= 2^20)
     return in <= snap ? u - in : kb - in <= snap ? u + kb - in : u;
   }
-  __device__ __forceinline__ int owner(int u) const {
-    int c = u * cuts / units;
-    while (c + 1 < cuts && at(c + 1) <= u) ++c;
-    while (c > 0 && at(c) > u) --c;
-    return c;
+  // The stretches that hold a tile's first and last unit, by a whole warp: 8 lanes look at the stretches around each.
+  __device__ __forceinline__ void owners(int tile, int& first, int& last) const {
+    const int lane = threadIdx.x & 31, u = (lane & 8) ? (tile + 1) * kb - 1 : tile * kb;
+    const int from = (int)((float)u * ((float)cuts / (float)units)) - 3, c = from + (lane & 7);
+    const uint32_t begun = __ballot_sync(0xFFFFFFFFu, lane < 16 && c < cuts && (c <= 0 || at(c) <= u));
+    first = __shfl_sync(0xFFFFFFFFu, from, 0) + __popc(begun & 0xFFu) - 1;
+    last = __shfl_sync(0xFFFFFFFFu, from, 8) + __popc(begun & 0xFF00u) - 1;
   }
 };
 
@@ -426,13 +429,19 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       else mbar_arrive_cluster(first_empty + at * 8);
     };
     // the place on the work is out of the registers while units are added up
-    Walk* const parked = reinterpret_cast<Walk*>(reinterpret_cast<uint8_t*>(scales + 2 * C::kScales) + e * 32);
-    static_assert(sizeof(Walk) <= 32, "space of a parked place");
+    struct Parked {
+      Walk w;
+      int first, last;  // the stretches of a cut tile's first and last piece
+    };
+    Parked* const parked = reinterpret_cast<Parked*>(reinterpret_cast<uint8_t*>(scales + 2 * C::kScales) + e * kParked);
+    static_assert(sizeof(Parked) <= kParked, "space of a parked place");
     while (ok && w.next(p)) {
       w.place(p, m, n);
       const bool live = (m * CG + (int)rank) * 128 + quarter * 32 < p.a.T;
       const int count = w.k1 - w.k0;
-      if (lane == 0) *parked = w;
+      int first = id, last = id;
+      if (count < p.kb) cuts.owners(w.tile - p.whole, first, last);
+      if (lane == 0) *parked = Parked{w, first, last};
       float2 acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
@@ -476,13 +485,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
       if (!ok) break;
       __syncwarp();
-      w = *parked;
+      w = parked->w;
+      first = parked->first;
+      const int pieces = parked->last - first + 1;
       __syncwarp();
       if (!live) continue;
       w.place(p, m, n);
       const int row0 = (m * CG + (int)rank) * 128 + quarter * 32, col0 = n * BN + part * 128;
       if (count < p.kb) {  // a piece: the last to finish adds the tile's pieces
-        const int first = cuts.owner((w.tile - p.whole) * p.kb), pieces = cuts.owner((w.tile - p.whole + 1) * p.kb - 1) - first + 1;
         const int index = id - first;
         const auto part_of = [&](int i) {  // the i-th piece: a stretch's piece at a tile's start, or its other one
           return reinterpret_cast<float4*>(p.parts + ((int64_t)((first + i) * CG + (int)rank) * 2 + (i == 0 ? 1 : 0)) * C::kPart) +
@@ -505,18 +515,19 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           }
         };
         int done = 0;
-        // Where the others are done already, this piece need not be written. (In the sum's order it has to be one of the
-        // first two, which may change places.)
-        if (lane == 0 && index < 2) done = load_acquire(ticket);
+        // Where the others are done already, this piece need not be written: looked up where no more work waits for this
+        // warp. (In the sum's order it has to be one of the first two, which may change places.)
+        if (lane == 0 && index < 2 && w.u >= w.u_end) done = load_acquire(ticket);
         done = __shfl_sync(0xFFFFFFFFu, done, 0);
         if (done == pieces - 1) {
           for (int i = 0; i < pieces; ++i)
             if (i != index) add(i, true);
         } else {
           float4* mine = part_of(index);
+          if (row0 + lane < p.a.T)
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            mine[c * 32] = make_float4(acc[2 * c].x, acc[2 * c].y, acc[2 * c + 1].x, acc[2 * c + 1].y);
+            for (int c = 0; c < 32; ++c)
+              mine[c * 32] = make_float4(acc[2 * c].x, acc[2 * c].y, acc[2 * c + 1].x, acc[2 * c + 1].y);
           __threadfence();
           __syncwarp();
           if (lane == 0) done = atomicAdd(ticket, 1);
@@ -560,7 +571,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
       }
     }
-    if (lane == 0) bulk_wait();
+    if (lane == 0) bulk_wait_read();  // shared memory goes away
     __syncwarp();
   } else {
     if constexpr (C::kMoveRegs) regs_down<72>();
@@ -683,6 +694,26 @@ bool matmul8_configure() {
   return cudaFuncSetAttribute(matmul8_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) == cudaSuccess;
 }
 
+// Into how many stretches the units of `left` tiles are cut: every tile into the same number of pieces, or all units into as
+// many stretches as there are CTAs (or pairs), whose borders then lie inside tiles. The estimates, in us, are of this card:
+// a unit takes what its products do or, of weights that stream from memory, its bytes' share; the pieces of a tile are written
+// and read again; and a stretch that goes on in a second tile stalls for its first piece's way out.
+template <class C>
+int matmul8_cuts(int left, int kb, int most) {
+  const auto cost = [&](int cuts) {
+    const int64_t units = (int64_t)left * kb;
+    const double stretch = (double)((units + cuts - 1) / cuts), each = std::max(C::kUnitUs, cuts * C::CG * (double)C::kB / 6.5e6);
+    const bool inside = cuts % left != 0;
+    const double pieces = inside ? kb / stretch + 1 : cuts / left;
+    return stretch * each + (pieces > 1 ? 2.0 + 0.6 * pieces : 0.0) + (inside ? 2.5 : 0.0);
+  };
+  int best = left;
+  for (int cuts = 2 * left; cuts <= most && cuts <= left * kb; cuts += left)
+    if (cost(cuts) < cost(best)) best = cuts;
+  if ((int64_t)left * kb >= most && cost(most) < cost(best)) best = most;
+  return best;
+}
+
 template <class C>
 int matmul8_launch(const moe_matmul8_ctx* ctx, const moe_matmul8_args& a, cudaStream_t stream) {
   MatmulParams p;
@@ -697,7 +728,7 @@ int matmul8_launch(const moe_matmul8_ctx* ctx, const moe_matmul8_args& a, cudaSt
   const int left = (int)(tiles % most);
   p.whole = (int)tiles - left;
   p.units = left * p.kb;
-  p.cuts = std::max(left ? 1 : 0, std::min(most, p.units / kMinUnits));
+  p.cuts = left ? matmul8_cuts<C>(left, p.kb, most) : 0;
   p.snap = p.cuts ? p.units / p.cuts / 16 : 0;
   p.a_rows = (int)std::min<int64_t>(128, (a.T + 7) / 8 * 8);
   p.stages = std::min(C::kMaxStages, (kSmemLimit - C::kFixed) / (p.a_rows * 128 + C::kB));
