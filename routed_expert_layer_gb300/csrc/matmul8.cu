@@ -273,7 +273,8 @@ struct MatmulParams {
 template <int CG_, int BN_, int DT_>
 struct MatmulCfg {
   static constexpr int CG = CG_, BN = BN_, DT = DT_;
-  static constexpr int kEpi = 4 * (BN / 128);      // epilogue warps
+  static constexpr int kEpi = 8;                   // epilogue warps: 32 rows and half of the columns each
+  static constexpr int kCols = BN / 2;
   static constexpr int kThreads = 128 + 32 * kEpi;
   static constexpr int kBlocks = BN / 128;         // blocks of W8's scales in a tile
   static constexpr int kBufs = 4;                  // products of 128 columns in tensor memory
@@ -285,10 +286,13 @@ struct MatmulCfg {
   static constexpr int kMaxStages = 12;
   static constexpr double kUnitUs = CG == 1 ? 0.25 : 0.5;  // a unit's time on the SM
   static constexpr int kScales = kChunk * (kScaleRow + BN / 128);  // floats of a chunk's scales
-  static constexpr int kFixed = 1024 + kStaging + 2 * kScales * 4 + kParked * kEpi + 512;
-  // Registers of the first warpgroup and of the epilogue's, where launching with an equal share gives the latter too few:
-  // 384 threads of 168 are 128 of 72 and 256 of 216.
-  static constexpr bool kMoveRegs = kThreads > 256;
+  // Shared memory. What the epilogue uses lies at constant places: addresses cost it no registers, and a spilled one in the
+  // units' loop costs more than the arithmetic there.
+  static constexpr int kScalesAt = 512, kParkedAt = kScalesAt + 2 * kScales * 4;
+  static constexpr int kStagingAt = (kParkedAt + kParked * kEpi + 1023) / 1024 * 1024, kStagesAt = kStagingAt + kStaging;
+  static constexpr int kFixed = 1024 + kStagesAt;
+  // Registers: 384 threads of 168. Of a pair's kernel the first 128 give theirs up: 88 for them and 208 for the epilogue.
+  static constexpr bool kMoveRegs = CG == 2;
 };
 constexpr int kSmemLimit = 232448;
 
@@ -375,14 +379,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   // the MMA reads 128 rows of A8 from a stage's start, whatever the stage holds: rows past a_rows are other
   // stages' and end in lanes that nobody reads
   const int a_bytes = p.a_rows * 128;
-  uint8_t* staging = smem;
-  uint8_t* sa = smem + C::kStaging;
-  uint8_t* sw = sa + (size_t)p.stages * a_bytes;
-  uint64_t* bar = reinterpret_cast<uint64_t*>(sw + (size_t)p.stages * C::kB);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem);
   uint64_t *full = bar, *empty = full + C::kMaxStages, *acc_full = empty + C::kMaxStages, *acc_empty = acc_full + C::kBufs;
   uint64_t *scale_full = acc_empty + C::kBufs, *scale_empty = scale_full + 2, *drain = scale_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  float* scales = reinterpret_cast<float*>(bar + 64);  // [2][kChunk][kScaleRow | BN / 128]
+  float* scales = reinterpret_cast<float*>(smem + C::kScalesAt);  // [2][kChunk][kScaleRow | kBlocks]
+  uint8_t* sa = smem + C::kStagesAt;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 1 ? 0 : cluster_rank();
@@ -393,7 +395,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     }
     for (int s = 0; s < C::kBufs; ++s) {
       mbar_init(&acc_full[s], 1);
-      mbar_init(&acc_empty[s], CG * 4);
+      mbar_init(&acc_empty[s], 8);  // 4 warps of both CTAs, or 8 of one
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&scale_full[s], 2);
@@ -418,10 +420,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   int m, n;
 
   if (warp >= 4) {
-    if constexpr (C::kMoveRegs) regs_up<216>();
-    const int e = warp - 4, quarter = warp & 3, part = e >> 2;
+    if constexpr (C::kMoveRegs) regs_up<208>();
+    const int e = warp - 4, quarter = warp & 3, part = e >> 2, block = CG == 1 ? 0 : part;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    uint8_t* stage = staging + e * 4096;
+    uint8_t* stage = smem + C::kStagingAt + e * 4096;
     uint32_t units = 0, chunks = 0;  // passed so far: their buffers and parities
     const uint32_t first_empty = CG == 1 ? 0 : cluster_addr(acc_empty, 0);
     const auto free_acc = [&](uint32_t at) {
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       Walk w;
       int first, last;  // the stretches of a cut tile's first and last piece
     };
-    Parked* const parked = reinterpret_cast<Parked*>(reinterpret_cast<uint8_t*>(scales + 2 * C::kScales) + e * kParked);
+    Parked* const parked = reinterpret_cast<Parked*>(smem + C::kParkedAt + e * kParked);
     static_assert(sizeof(Parked) <= kParked, "space of a parked place");
     while (ok && w.next(p)) {
       w.place(p, m, n);
@@ -442,27 +444,27 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       int first = id, last = id;
       if (count < p.kb) cuts.owners(w.tile - p.whole, first, last);
       if (lane == 0) *parked = Parked{w, first, last};
-      float2 acc[64];
+      float2 acc[C::kCols / 2];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
+      for (int i = 0; i < C::kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
 #pragma unroll 1
       for (int k = 0; k < count; ++k, ++units) {
-        const int x = k & (kChunk - 1), buf = units % C::kDeep * C::kBlocks + part;
+        const int x = k & (kChunk - 1), buf = units % C::kDeep * C::kBlocks + block;
         if (x == 0) ok = wait_warp(&scale_full[chunks & 1], chunks >> 1 & 1, p.err);
         const float* sc = scales + (chunks & 1) * C::kScales;
-        const float s = sc[x * kScaleRow + quarter * 32 + lane] * sc[kChunk * kScaleRow + x * C::kBlocks + part];
+        const float s = sc[x * kScaleRow + quarter * 32 + lane] * sc[kChunk * kScaleRow + x * C::kBlocks + block];
         ok = ok && wait_warp(&acc_full[buf], units / C::kDeep & 1, p.err);
         if (!ok) break;
         tc_fence_after();
         if (live) {
-          const uint32_t from = tmem + lane_base + buf * 128;
+          const uint32_t from = tmem + lane_base + buf * 128 + (CG == 1 ? part * C::kCols : 0);
           const float2 s2 = make_float2(s, s);
           uint32_t v[2][32];  // a load runs under the arithmetic of the one before
           tmem_ld32(from, v[0]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < C::kCols / 32; ++c) {
             tmem_wait_ld32(v[c & 1]);
-            if (c < 3) {
+            if (c + 1 < C::kCols / 32) {
               tmem_ld32(from + (c + 1) * 32, v[(c + 1) & 1]);
             } else {
               tc_fence_before();
@@ -491,18 +493,18 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       __syncwarp();
       if (!live) continue;
       w.place(p, m, n);
-      const int row0 = (m * CG + (int)rank) * 128 + quarter * 32, col0 = n * BN + part * 128;
+      const int row0 = (m * CG + (int)rank) * 128 + quarter * 32, col0 = n * BN + part * C::kCols;
       if (count < p.kb) {  // a piece: the last to finish adds the tile's pieces
         const int index = id - first;
         const auto part_of = [&](int i) {  // the i-th piece: a stretch's piece at a tile's start, or its other one
           return reinterpret_cast<float4*>(p.parts + ((int64_t)((first + i) * CG + (int)rank) * 2 + (i == 0 ? 1 : 0)) * C::kPart) +
-                 e * 1024 + lane;
+                 e * (C::kCols * 8) + lane;
         };
         int32_t* ticket = p.tickets + ((w.tile - p.whole) * CG + (int)rank) * C::kEpi + e;
         const auto add = [&](int i, bool to_sum) {
           const float4* from = part_of(i);
 #pragma unroll
-          for (int c = 0; c < 32; c += 16) {
+          for (int c = 0; c < C::kCols / 4; c += 16) {
             float4 v[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = __ldcg(from + (c + j) * 32);
@@ -526,7 +528,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           float4* mine = part_of(index);
           if (row0 + lane < p.a.T)
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
+            for (int c = 0; c < C::kCols / 4; ++c)
               mine[c * 32] = make_float4(acc[2 * c].x, acc[2 * c].y, acc[2 * c + 1].x, acc[2 * c + 1].y);
           __threadfence();
           __syncwarp();
@@ -540,7 +542,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
       // 64 columns at a time through shared memory: a row of 128 bytes per lane, 16-byte pieces swizzled by row
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < C::kCols / 64; ++h) {
         const int col = col0 + h * 64;
         if (col >= p.a.N) break;
         if (lane == 0) bulk_wait_read();
@@ -574,7 +576,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     if (lane == 0) bulk_wait_read();  // shared memory goes away
     __syncwarp();
   } else {
-    if constexpr (C::kMoveRegs) regs_down<72>();
+    if constexpr (C::kMoveRegs) regs_down<88>();
+    uint8_t* sw = sa + (size_t)p.stages * a_bytes;
     if (warp == 0) {
       if (elect_one()) {
         uint32_t s = 0, turn = 0;
