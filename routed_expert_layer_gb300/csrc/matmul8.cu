@@ -284,7 +284,7 @@ struct MatmulCfg {
   static_assert(BN == 128 * CG, "each CTA of a tile loads 128 rows of W8");
   static constexpr int kStaging = kEpi * 4096;
   static constexpr int kMaxStages = 12;
-  static constexpr double kUnitUs = CG == 1 ? 0.25 : 0.5;  // a unit's time on the SM
+  static constexpr double kUnitUs = CG == 1 ? 0.34 : 0.54;  // a unit's time on the SM
   static constexpr int kScales = kChunk * (kScaleRow + BN / 128);  // floats of a chunk's scales
   // Shared memory. What the epilogue uses lies at constant places: addresses cost it no registers, and a spilled one in the
   // units' loop costs more than the arithmetic there.
@@ -411,13 +411,23 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   else cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_entry();
 
   const Cuts cuts{p.units, p.cuts, p.snap, p.kb};
   const int id = (int)(blockIdx.x / CG);
   Walk w(p, cuts, id, (int)(gridDim.x / CG));
   bool ok = true;
   int m, n;
+  // While the kernel before this one ends, the first stages' weights come as far as L2 (which stays right whoever writes them).
+  if (warp == 0 && elect_one()) {
+    Walk ahead = w;
+    if (ahead.next(p)) {
+      ahead.place(p, m, n);
+      for (int k = ahead.k0; k < min(ahead.k1, ahead.k0 + p.stages); ++k)
+        for (int h = 0; h < C::kBlocks; ++h) prefetch_2d(&map_w, k * 128, n * BN + (int)rank * (128 / CG) + h * 128);
+    }
+  }
+  __syncwarp();
+  pdl_entry();
 
   if (warp >= 4) {
     if constexpr (C::kMoveRegs) regs_up<208>();
@@ -697,41 +707,56 @@ bool matmul8_configure() {
   return cudaFuncSetAttribute(matmul8_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) == cudaSuccess;
 }
 
-// Into how many stretches the units of `left` tiles are cut: every tile into the same number of pieces, or all units into as
-// many stretches as there are CTAs (or pairs), whose borders then lie inside tiles. The estimates, in us, are of this card:
-// a unit takes what its products do or, of weights that stream from memory, its bytes' share; the pieces of a tile are written
-// and read again; and a stretch that goes on in a second tile stalls for its first piece's way out.
+// How a product is shared out: tiles in whole rounds over the CTAs (or pairs), and the stretches into which the units of the
+// tiles left over are cut: every tile into the same number of pieces, or all units into as many stretches as there are CTAs,
+// whose borders then lie inside tiles. The estimates, in us, are of this card: a unit takes what its products do or, of weights
+// that stream from memory, its bytes' share; the pieces of a tile are written and read again; and a stretch that goes on in
+// a second tile stalls for its first piece's way out. (517 x 1811 x 7152: 75 tiles of single CTAs in two pieces each 19.7 us,
+// 24 of pairs in three 23.9; 1024 x 14336 x 7168 119 and 90.)
+struct MatmulPlan {
+  int64_t m_tiles, n_tiles;
+  int most, left, cuts;
+  double us;
+};
 template <class C>
-int matmul8_cuts(int left, int kb, int most) {
-  const auto cost = [&](int cuts) {
-    const int64_t units = (int64_t)left * kb;
-    const double stretch = (double)((units + cuts - 1) / cuts), each = std::max(C::kUnitUs, cuts * C::CG * (double)C::kB / 6.5e6);
-    const bool inside = cuts % left != 0;
-    const double pieces = inside ? kb / stretch + 1 : cuts / left;
+MatmulPlan matmul8_plan(const moe_matmul8_args& a, int sm_count) {
+  MatmulPlan p;
+  p.m_tiles = ((int64_t)a.T + 128 * C::CG - 1) / (128 * C::CG);
+  p.n_tiles = ((int64_t)a.N + C::BN - 1) / C::BN;
+  p.most = sm_count / C::CG;
+  const int64_t tiles = p.m_tiles * p.n_tiles, kb = (a.K + 127) / 128;
+  p.left = (int)(tiles % p.most);
+  p.us = (double)(tiles / p.most * kb) * C::kUnitUs;
+  p.cuts = 0;
+  if (p.left == 0) return p;
+  const int64_t units = p.left * kb;
+  const auto cost = [&](int64_t cuts) {
+    const double stretch = (double)((units + cuts - 1) / cuts);
+    const double each = std::max(C::kUnitUs, (double)(cuts * C::CG) * C::kB / (double)p.m_tiles / 6.5e6);
+    const bool inside = cuts % p.left != 0;
+    const double pieces = inside ? (double)kb / stretch + 1 : (double)(cuts / p.left);
     return stretch * each + (pieces > 1 ? 2.0 + 0.6 * pieces : 0.0) + (inside ? 2.5 : 0.0);
   };
-  int best = left;
-  for (int cuts = 2 * left; cuts <= most && cuts <= left * kb; cuts += left)
-    if (cost(cuts) < cost(best)) best = cuts;
-  if ((int64_t)left * kb >= most && cost(most) < cost(best)) best = most;
-  return best;
+  p.cuts = p.left;
+  for (int64_t cuts = 2 * p.left; cuts <= p.most && cuts <= units; cuts += p.left)
+    if (cost(cuts) < cost(p.cuts)) p.cuts = (int)cuts;
+  if (units >= p.most && cost(p.most) < cost(p.cuts)) p.cuts = p.most;
+  p.us += cost(p.cuts);
+  return p;
 }
 
 template <class C>
-int matmul8_launch(const moe_matmul8_ctx* ctx, const moe_matmul8_args& a, cudaStream_t stream) {
+int matmul8_launch(const moe_matmul8_ctx* ctx, const moe_matmul8_args& a, const MatmulPlan& plan, cudaStream_t stream) {
   MatmulParams p;
   p.a = a;
   p.kb = (a.K + 127) / 128;
-  const int64_t m_tiles = ((int64_t)a.T + 128 * C::CG - 1) / (128 * C::CG), n_tiles = ((int64_t)a.N + C::BN - 1) / C::BN;
-  const int64_t tiles = m_tiles * n_tiles;
+  const int64_t tiles = plan.m_tiles * plan.n_tiles;
   if (tiles * p.kb >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
-  p.m_tiles = (int)m_tiles;
-  p.n_tiles = (int)n_tiles;
-  const int most = ctx->sm_count / C::CG;  // CTAs or pairs
-  const int left = (int)(tiles % most);
-  p.whole = (int)tiles - left;
-  p.units = left * p.kb;
-  p.cuts = left ? matmul8_cuts<C>(left, p.kb, most) : 0;
+  p.m_tiles = (int)plan.m_tiles;
+  p.n_tiles = (int)plan.n_tiles;
+  p.whole = (int)tiles - plan.left;
+  p.units = plan.left * p.kb;
+  p.cuts = plan.cuts;
   p.snap = p.cuts ? p.units / p.cuts / 16 : 0;
   p.a_rows = (int)std::min<int64_t>(128, (a.T + 7) / 8 * 8);
   p.stages = std::min(C::kMaxStages, (kSmemLimit - C::kFixed) / (p.a_rows * 128 + C::kB));
@@ -744,7 +769,7 @@ int matmul8_launch(const moe_matmul8_ctx* ctx, const moe_matmul8_args& a, cudaSt
       !make_map2(&mw, a.w8, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.N, a.K, a.w8_stride, 128 / C::CG) ||
       (p.tma_out && !make_map2(&mo, a.out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.T, a.N, a.out_stride, 32)))
     return MOE_ERR_CUDA;
-  const int ctas = (p.whole ? most : p.cuts) * C::CG;
+  const int ctas = (p.whole ? plan.most : p.cuts) * C::CG;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -769,7 +794,9 @@ using PairMatmul = MatmulCfg<2, 256, DT>;
 
 template <int DT>
 int matmul8_by_rows(const moe_matmul8_ctx* ctx, const moe_matmul8_args& a, cudaStream_t s) {
-  return a.T <= 128 ? matmul8_launch<StreamMatmul<DT>>(ctx, a, s) : matmul8_launch<PairMatmul<DT>>(ctx, a, s);
+  const MatmulPlan one = matmul8_plan<StreamMatmul<DT>>(a, ctx->sm_count), two = matmul8_plan<PairMatmul<DT>>(a, ctx->sm_count);
+  if (a.T <= 128 || one.us < two.us) return matmul8_launch<StreamMatmul<DT>>(ctx, a, one, s);
+  return matmul8_launch<PairMatmul<DT>>(ctx, a, two, s);
 }
 
 // Bytes a strided [rows][width] tensor spans.
