@@ -159,7 +159,16 @@ struct Work {
   int64_t head_cost;       // cost of one key head of the request
   int64_t base, at, cost;  // axis: start of the head, start and length of the item
 
-  template <int QT>
+  // Whether the request's new tokens see one another by their masks (else in a row, as in all calls without masks).
+  template <bool TREE>
+  __device__ __forceinline__ bool by_mask(const AttnParams& p) const { return TREE && n_new <= 32 * p.words; }
+  // The length of the first n items: each reads the keys up to its last row's, or by masks all of them.
+  template <int QT, bool TREE>
+  __device__ __forceinline__ int64_t length(const AttnParams& p, int64_t n) const {
+    const int64_t each = fixed + max(ctx, 0), st = QT * p.tpt;
+    return by_mask<TREE>(p) ? n * (each + n_new) : n * each + st * (n * (n + 1) / 2);
+  }
+  template <int QT, bool TREE>
   __device__ __forceinline__ bool load(const AttnParams& p, int request) {  // false: rows outside q, or keys past the table
     b = request;
     const int s = p.a.q_start[b], e = p.a.q_start[b + 1], most = p.a.W << p.p_shift, len = p.a.kv_lens[b];
@@ -172,16 +181,16 @@ struct Work {
     n_items = (n_new + st - 1) / st;
     const int64_t n = n_items;
     fixed = item_cost<QT>(min(n_new, st) * p.G);
-    head_cost = n * (fixed + max(ctx, 0)) + st * (n * (n - 1) / 2) + n_new;
+    head_cost = by_mask<TREE>(p) ? n * (fixed + max(ctx, 0) + n_new) : n * (fixed + max(ctx, 0)) + st * (n * (n - 1) / 2) + n_new;
     return ok && len <= most;
   }
-  template <int QT>
+  template <int QT, bool TREE>
   __device__ __forceinline__ void set_item(const AttnParams& p, int64_t before) {
     at = base + before;
-    cost = fixed + max(ctx, 0) + min((i + 1) * QT * p.tpt, n_new);
+    cost = fixed + max(ctx, 0) + (by_mask<TREE>(p) ? n_new : min((i + 1) * QT * p.tpt, n_new));
   }
   // The item at x, by a whole warp (every lane gets it).
-  template <int QT>
+  template <int QT, bool TREE>
   __device__ __forceinline__ void seek(const AttnParams& p, const int64_t* runs, int seg, int64_t x) {
     static_assert(kRuns == 128, "four runs per lane");
     const int lane = threadIdx.x & 31;
@@ -189,48 +198,42 @@ struct Work {
     lo += __popc(__ballot_sync(0xFFFFFFFFu, runs[lo + (lane & 3)] <= x) & 15) - 1;
     int64_t acc = runs[lo];
     int r = lo * seg;
-    load<QT>(p, r);
+    load<QT, TREE>(p, r);
     while (x - acc >= (int64_t)p.a.Hkv * head_cost && r + 1 < p.a.B) {
       acc += (int64_t)p.a.Hkv * head_cost;
-      load<QT>(p, ++r);
+      load<QT, TREE>(p, ++r);
     }
     h = (int)div_floor(x - acc, head_cost);
     base = acc + h * head_cost;
-    const int64_t rest = x - base, each = fixed + max(ctx, 0), st = QT * p.tpt;
+    const int64_t rest = x - base;
     int hi = n_items;
     lo = 0;
     while (hi - lo > 1) {  // the last group that starts at or before rest
       const int64_t mid = (lo + hi) >> 1;
-      if (mid * each + st * (mid * (mid + 1) / 2) <= rest) lo = (int)mid;
+      if (length<QT, TREE>(p, mid) <= rest) lo = (int)mid;
       else hi = (int)mid;
     }
     i = lo;
-    set_item<QT>(p, i * each + st * ((int64_t)i * (i + 1) / 2));
+    set_item<QT, TREE>(p, length<QT, TREE>(p, i));
   }
-  template <int QT>
+  template <int QT, bool TREE>
   __device__ __forceinline__ void next(const AttnParams& p) {
     if (i + 1 < n_items) {
       const int64_t before = at - base + cost;
       ++i;
-      set_item<QT>(p, before);
+      set_item<QT, TREE>(p, before);
       return;
     }
     i = 0;
     base += head_cost;
     if (++h == p.a.Hkv) {
       h = 0;
-      do load<QT>(p, b + 1);
+      do load<QT, TREE>(p, b + 1);
       while (n_items == 0 && b + 1 < p.a.B);
     }
-    set_item<QT>(p, 0);
+    set_item<QT, TREE>(p, 0);
   }
 };
-
-// Whether the request's new tokens see one another by their masks (else in a row, as in all calls without masks).
-template <bool TREE>
-__device__ __forceinline__ bool by_mask(const AttnParams& p, const Work& w) {
-  return TREE && w.n_new <= 32 * p.words;
-}
 
 // Which of 32 new tokens a row with these mask words sees, the first of them `rel` (cached tokens lie below 0: all seen).
 __device__ __forceinline__ uint32_t mask_bits(const uint32_t* row, int words, int n_new, int rel) {
@@ -256,7 +259,7 @@ struct Piece {
   bool split;
   __device__ __forceinline__ Piece(const AttnParams& p, const Work& w, const Axis& ax) {
     const int tok = w.i * QT * p.tpt;
-    const bool tree = by_mask<TREE>(p, w);
+    const bool tree = w.by_mask<TREE>(p);
     kv_end = max(0, w.ctx + (tree ? w.n_new : min(tok + QT * p.tpt, w.n_new)));
     first_lim = tree ? max(w.ctx, 0) : w.ctx + tok + 1;
     const int nt = (kv_end + BN - 1) / BN;
@@ -408,7 +411,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
   if (warp < kRuns / 32) {
     for (int b = threadIdx.x * seg; b < min(B, (int)(threadIdx.x + 1) * seg); ++b) {
       Work one{};
-      if (!one.load<QT>(p, b) && blockIdx.x == 0) atomicOr(p.err, kErrIndex);
+      if (!one.load<QT, TREE>(p, b) && blockIdx.x == 0) atomicOr(p.err, kErrIndex);
       mine += (int64_t)p.a.Hkv * one.head_cost;
     }
     upto = mine;
@@ -440,11 +443,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
   if (threadIdx.x == 0) *parked_axis = ax;
   __syncthreads();
   Work w{};
-  if (ax.x0 < ax.x1) w.seek<QT>(p, runs, seg, ax.x0);
+  if (ax.x0 < ax.x1) w.seek<QT, TREE>(p, runs, seg, ax.x0);
   bool more = ax.x0 < ax.x1, ok = true;
   auto advance = [&] {
     more = ok && w.at + w.cost < ax.x1;
-    if (more) w.next<QT>(p);
+    if (more) w.next<QT, TREE>(p);
   };
 
   if (warp == 0) {
@@ -680,7 +683,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
     };
     Work* const place = reinterpret_cast<Work*>(reinterpret_cast<uint8_t*>(parked) + 64 * (warp - 4));
     while (more) {
-      int t0, t_end, lim, tile_lim;
+      int t0, t_end, lim = 0, tile_lim;
       bool live, warp_live;
       {
         const Piece<QT, BN, TREE> pc(p, w, ax);
@@ -693,9 +696,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         t_end = q == 0 ? pc.tq1[0] : pc.tq1[QT - 1];
         live = rt < n_tok;
         warp_live = quarter * 32 < n_tok * p.G;
-        const bool tree = by_mask<TREE>(p, w);
-        lim = tree ? pc.kv_end : w.ctx + tok + rt + 1;       // keys this row sees, or may see by its mask (live rows)
+        const bool tree = w.by_mask<TREE>(p);
+        if constexpr (!TREE) lim = w.ctx + tok + rt + 1;    // keys this row sees (live rows; with masks worked out where needed)
         tile_lim = tree ? pc.first_lim : w.ctx + tok + 1;   // keys every row of the tile sees
+        if (tree && live) {  // the row's mask comes near while the first scores are computed
+          uint32_t unused;
+          asm volatile("ld.global.u32 %0, [%1];" : "=r"(unused) : "l"(p.mask + (int64_t)(w.q0 + tok + rt) * p.words));
+        }
       }
       __syncwarp();
       if (lane == 0) *place = w;
@@ -709,11 +716,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         if (warp_live) {
           const int64_t key0 = (int64_t)t * BN;
           if (key0 + BN > tile_lim) {  // hide keys in place: few tiles need it, so it is kept out of the code of the others
-            const int see = (int)max(min((int64_t)lim - key0, (int64_t)BN), (int64_t)0);
             if constexpr (TREE) {  // what the masks need waits in the parked place
-              const int n_new = place->n_new, rel0 = (int)key0 - place->ctx;
+              const int n_new = place->n_new, rel0 = (int)key0 - place->ctx, token = (place->i * QT + q) * p.tpt + rt;
               const bool tree = live && n_new <= 32 * p.words;
-              const uint32_t* row = p.mask + (int64_t)(place->q0 + (place->i * QT + q) * p.tpt + rt) * p.words;
+              const int see = max(min(token + 1 - rel0, BN), 0);
+              const uint32_t* row = p.mask + (int64_t)(place->q0 + token) * p.words;
 #pragma unroll 1
               for (int c = 0; c < BN; c += 32) {
                 const int left = see - c;
@@ -729,6 +736,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
                 tmem_st32(ts + c, v);
               }
             } else {
+              const int see = (int)max(min((int64_t)lim - key0, (int64_t)BN), (int64_t)0);
 #pragma unroll 1
               for (int c = 0; c < BN; c += 32) {
                 uint32_t v[32];
@@ -806,6 +814,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
       w = *place;
       const Piece<QT, BN, TREE> pc(p, w, *parked_axis);
       const int tok = (w.i * QT + q) * p.tpt;       // the tile's first token
+      if constexpr (TREE) lim = w.by_mask<TREE>(p) ? pc.kv_end : w.ctx + tok + rt + 1;  // the row's last key, or by its mask any
       const int n_tok = min(p.tpt, w.n_new - tok);  // its tokens (<= 0: no such tile)
       if (pc.tiles()) {
         ok = warp_wait(&ofull[q], on & 1, p.err);
@@ -846,7 +855,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
                 if (!((note[rel >> 5] | note[8 + (rel >> 5)]) >> (rel & 31) & 1)) continue;
                 const int key = pc.first_lim + rel, col = key >> p.p_shift;
                 if constexpr (TREE) {
-                  if (by_mask<TREE>(p, w) && !(mask_bits(p.mask + n_row * p.words, p.words, w.n_new, key - w.ctx) & 1)) continue;
+                  if (w.by_mask<TREE>(p) && !(mask_bits(p.mask + n_row * p.words, p.words, w.n_new, key - w.ctx) & 1)) continue;
                 }
                 const int id = p.a.block_table[w.b * p.a.table_stride + col];
                 const uint16_t* v = (const uint16_t*)p.a.v_cache + id * p.a.vc_page +
