@@ -257,8 +257,8 @@ MOE_API int moe_tree_accept(void* stream, const moe_tree_accept_args* a);
  * (with group 128): blocks of 128 x 128, as moe_matmul8_forward takes weights. Blocks at the ends may be
  * smaller. scales [ceil(T / rows)][ceil(H / group)], contiguous. A block of zeros has s = 0 and zeros; a NaN
  * makes its block's scale and values NaN; an infinity its scale infinite, itself NaN and the
- * others 0. x [T][H] of dtype, out8 [T][H], rows strided; out8 and scales share no byte with x or
- * one another. */
+ * others 0. x [T][H] of dtype, out8 [T][H], rows strided; the memory that x, out8 and scales span, from first
+ * to last element, does not overlap. 1 <= H <= 2^30. */
 typedef struct {
   const void* x;
   uint8_t* out8;
@@ -275,8 +275,9 @@ MOE_API int moe_quantize8(void* stream, const moe_quantize8_args* a);
  * [ceil(N / 128)][ceil(K / 128)]; a_scales [T][a_blocks], a_blocks = ceil(K / 128), or 1 for a
  * scale per row. The scales are as moe_add_rmsnorm (group 0, 128) and moe_quantize8 write them;
  * rows of every tensor may be strided. K a multiple of 16, a8 and w8 16-byte aligned with row strides that
- * are multiples of 16; out is aligned to its elements and shares no byte with an input.
- * T, N >= 0; T or N 0: nothing is done. 16 <= K <= 2^20. */
+ * are multiples of 16; out is aligned to its elements. The memory from out's first to its last element
+ * overlaps no input's.
+ * 0 <= T, N <= 2^30 (T or N 0: nothing is done), 16 <= K <= 2^20. */
 typedef struct {
   const uint8_t* a8;
   const float* a_scales;

@@ -815,7 +815,7 @@ int matmul8_check(const moe_matmul8_args* a) {
     return MOE_ERR_INVALID_ARG;
   const int blocks = (a->K + 127) / 128;
   if (a->a_blocks != blocks && a->a_blocks != 1) return MOE_ERR_INVALID_ARG;
-  if (a->K > 1 << 20) return MOE_ERR_UNSUPPORTED;
+  if (a->K > 1 << 20 || a->T > 1 << 30 || a->N > 1 << 30) return MOE_ERR_UNSUPPORTED;
   if (a->T == 0 || a->N == 0) return MOE_OK;
   if (!a->a8 || !a->w8 || !a->a_scales || !a->w_scales || !a->out || !is_aligned(a->a8, 16) || !is_aligned(a->w8, 16) ||
       !is_aligned(a->a_scales, 4) || !is_aligned(a->w_scales, 4) || !is_aligned(a->out, 2))
@@ -844,6 +844,7 @@ extern "C" {
 int moe_quantize8(void* stream, const moe_quantize8_args* a) {
   if (!a || a->T < 0 || a->H < 1 || (a->dtype != MOE_DT_BF16 && a->dtype != MOE_DT_F16)) return MOE_ERR_INVALID_ARG;
   if (!(a->group == 128 && (a->rows == 1 || a->rows == 128)) && !(a->group == 0 && a->rows == 1)) return MOE_ERR_INVALID_ARG;
+  if (a->H > 1 << 30) return MOE_ERR_UNSUPPORTED;
   if (a->T == 0) return MOE_OK;
   if (!a->x || !a->out8 || !a->scales || !is_aligned(a->x, 2) || !is_aligned(a->scales, 4)) return MOE_ERR_INVALID_ARG;
   if (a->T > 1 && (a->x_stride < a->H || a->out8_stride < a->H)) return MOE_ERR_INVALID_ARG;

@@ -19,6 +19,7 @@ constexpr int kTreeNodes = 32 * MOE_TREE_WORDS;
 __global__ void __launch_bounds__(kTreeNodes) tree_plan_kernel(const moe_tree_plan_args a, int per_shift) {
   __shared__ uint32_t s_mask[MOE_TREE_WORDS][kTreeNodes];
   __shared__ int16_t s_up[kTreeNodes];
+  __shared__ int s_chunk[kTreeNodes / 32][3];  // of each of the block's requests that is a chunk: tokens, first row, context
   pdl_entry();
   const int tid = threadIdx.x, per = 1 << per_shift, t = tid & (per - 1), g0 = tid - t, W = a.words;
   const int64_t request = (int64_t)blockIdx.x * (kTreeNodes >> per_shift) + (tid >> per_shift);
@@ -40,12 +41,13 @@ __global__ void __launch_bounds__(kTreeNodes) tree_plan_kernel(const moe_tree_pl
   uint32_t mask[MOE_TREE_WORDS];
 #pragma unroll
   for (int w = 0; w < MOE_TREE_WORDS; ++w) mask[w] = t >> 5 == w ? 1u << (t & 31) : 0;
-  if (!tree) {
-    for (int i = t; i < n; i += per) {
-      if (a.parents[start + i] != i - 1) bad |= kErrPlan;
-      a.positions[start + i] = ctx + i;
-    }
-  } else if (t < n) {
+  if (t == 0) {
+    int* c = s_chunk[tid >> per_shift];
+    c[0] = tree ? 0 : n;
+    c[1] = start;
+    c[2] = ctx;
+  }
+  if (tree && t < n) {
     up = a.parents[start + t];
     if (up < -1 || up >= t) {
       up = -1;
@@ -74,6 +76,15 @@ __global__ void __launch_bounds__(kTreeNodes) tree_plan_kernel(const moe_tree_pl
     }
     up = next;
   }
+  // chunks by the whole block (the loop above has synchronised it)
+  for (int g = 0; g < kTreeNodes >> per_shift; ++g) {
+    const int tokens = s_chunk[g][0], row = s_chunk[g][1], from = s_chunk[g][2];
+#pragma unroll 4
+    for (int i = tid; i < tokens; i += kTreeNodes) {
+      if (a.parents[row + i] != i - 1) bad |= kErrPlan;
+      a.positions[row + i] = from + i;
+    }
+  }
   if (tree && t < n) {
     int depth = -1;
 #pragma unroll
@@ -91,14 +102,16 @@ __global__ void __launch_bounds__(kTreeNodes) tree_plan_kernel(const moe_tree_pl
 
 constexpr int kAcceptThreads = 256;
 constexpr int kMoves = 4;  // rows a thread has in flight
+constexpr int kNodesHeld = 512;  // nodes of a request that are walked in shared memory
 
 struct AcceptParams {
   moe_tree_accept_args a;
   int p_shift;
 };
 
-// Every block of a request walks down the tree for itself (its first warp, 32 nodes at a time), then moves its share of
-// the pieces of PE elements. A thread moves a piece of all rows, in the order of the path and in batches that are
+// Every block of a request walks down the tree for itself (its first warp, 32 nodes at a time; a step's three loads one after
+// another are what bounds small calls, so the nodes are brought to shared memory at once), then moves its share of the
+// pieces of PE elements. A thread moves a piece of all rows, in the order of the path and in batches that are
 // read before they are written: a row's source is never before its destination, and sources grow, so no row is
 // overwritten before it is read.
 template <typename Piece, int PE>
@@ -107,14 +120,26 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const __gri
   __shared__ int s_path[kTreeNodes];
   __shared__ int2 s_src[kTreeNodes], s_dst[kTreeNodes];  // page and row of the rows that move
   __shared__ int s_moves;
+  __shared__ int s_parent[kNodesHeld], s_token[kNodesHeld], s_target[kNodesHeld];
   pdl_entry();
   const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.y;
   const int start = a.q_start[b], end = a.q_start[b + 1], ctx = a.ctx_lens[b];
   const bool first_block = blockIdx.x == 0;
+  const bool inside = start >= 0 && end >= start && end <= a.N;
+  const int n = inside ? end - start : 0;
+  const bool held = n <= kNodesHeld;
+  if (held)
+    for (int i = tid; i < n; i += kAcceptThreads) {
+      s_parent[i] = a.parents[start + i];
+      s_token[i] = a.tokens[start + i];
+      s_target[i] = a.targets[start + i];
+    }
+  __syncthreads();
   if (tid < 32) {
     uint32_t bad = 0;
-    const bool inside = start >= 0 && end >= start && end <= a.N;
-    const int n = inside ? end - start : 0;
+    const int* parents = held ? s_parent : a.parents + start;
+    const int* tokens = held ? s_token : a.tokens + start;
+    const int* targets = held ? s_target : a.targets + start;
     if (!inside) bad |= kErrIndex;
     int c = n ? 1 : 0;
     if (a.certain && n) {
@@ -126,12 +151,12 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const __gri
     }
     int cur = c - 1, count = 0, target = -1;
     while (n) {
-      target = a.targets[start + cur];
+      target = targets[cur];
       if (count == a.depth) break;
       int child = -1;
       for (int j0 = cur + 1; j0 < n && child < 0; j0 += 32) {
         const int j = j0 + lane;
-        const bool hit = j < n && a.parents[start + j] == cur && a.tokens[start + j] == target;
+        const bool hit = j < n && parents[j] == cur && tokens[j] == target;
         const uint32_t hits = __ballot_sync(0xFFFFFFFFu, hit);
         if (hits) child = j0 + __ffs(hits) - 1;
       }

@@ -77,7 +77,7 @@ def quantize_args(**kw):
     (dict(x=0), BAD), (dict(out8=0), BAD), (dict(scales=0), BAD), (dict(x=A + 1), BAD), (dict(scales=C + 2), BAD), (dict(T=-1), BAD),
     (dict(H=0), BAD), (dict(dtype=2), BAD), (dict(group=64), BAD), (dict(rows=2), BAD), (dict(group=0, rows=128), BAD),
     (dict(x_stride=255), BAD), (dict(out8_stride=255), BAD), (dict(out8=A + 100), BAD), (dict(scales=A + 2044), BAD), (dict(out8=C - 1000), BAD),
-    (dict(T=0, x=0), OK),
+    (dict(T=0, x=0), OK), (dict(H=(1 << 30) + 1, x_stride=1 << 31, out8_stride=1 << 31), UNSUP),
 ])
 def test_quantize_refusals(L, kw, status):
     assert L.moe_quantize8(None, quantize_args(**kw)) == status

@@ -84,6 +84,19 @@ def test_tree_plan(words, B):
     assert mask == want[1]
 
 
+@pytest.mark.parametrize("words", [1, 3, 8])
+def test_tree_plan_long_chunks(words):
+    """Prompts of thousands of tokens beside trees; one that is no chain in its last token."""
+    r = random.Random(words)
+    parents = [dref.random_tree(r, 20), list(range(-1, 4999)), dref.random_tree(r, 31), [], list(range(-1, 700)), [-1]]
+    ctx = [3, 70000, 0, 5, 12, 1]
+    pos, mask, err = run_plan(parents, ctx, words, extra=2)
+    assert err == 0 and (pos, mask) == want_plan(parents, ctx, words, extra=2)
+    parents[1][-1] = 7
+    pos, mask, err = run_plan(parents, ctx, words)
+    assert err == rel.MOE_OPS_ERR_PLAN and (pos, mask) == want_plan(parents, ctx, words)
+
+
 def test_tree_plan_bad_input():
     """A parent that is not before its node counts as -1, a long request that is no chain as a chain, a negative
     context as 0; a request outside the rows is skipped. Each raises its bit, and the others are as ever."""
@@ -369,7 +382,7 @@ class Drafts:
 @pytest.mark.parametrize("sizes,layers,Hkv,D,P,depth,dtype", [
     ([1], 1, 1, 64, 16, 1, BF16), ([25], 1, 8, 128, 64, 6, BF16), ([60] * 7 + [0, 1, 2], 3, 2, 128, 16, 8, F16),
     ([300, 40, 33], 2, 4, 64, 32, 12, BF16), ([64] * 60, 5, 1, 128, 16, 5, BF16), ([17, 90], 2, 3, 33, 16, 20, F16),
-    ([12] * 3, 40, 8, 128, 4, 7, BF16), ([256], 1, 1, 1, 1, 256, F16),
+    ([12] * 3, 40, 8, 128, 4, 7, BF16), ([256], 1, 1, 1, 1, 256, F16), ([513, 1200], 1, 2, 64, 64, 30, BF16),
 ])
 def test_tree_accept(sizes, layers, Hkv, D, P, depth, dtype):
     moved = 0
