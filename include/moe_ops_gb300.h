@@ -10,7 +10,8 @@
  * (moe_attn_forward: of the handle's device), nothing allocated by a call, nothing
  * synchronised, every call may be captured in a CUDA graph, kernels never trap. Every kernel
  * here is launched with programmatic stream serialisation, waits for the kernel before it
- * before it touches memory, and lets the next kernel launch early: a following kernel that
+ * before it touches memory (moe_matmul8_forward asks for its first weights to be brought into L2 before
+ * that, and reads them after), and lets the next kernel launch early: a following kernel that
  * is itself launched with that attribute must wait on its grid dependency
  * (griddepcontrol.wait) before it reads these outputs, as for moe_forward.
  * 16-bit types: `dtype` is MOE_DT_BF16 or MOE_DT_F16 for every 16-bit tensor of a call.

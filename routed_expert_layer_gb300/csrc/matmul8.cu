@@ -544,6 +544,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         // warp. (In the sum's order it has to be one of the first two, which may change places.)
         if (lane == 0 && index < 2 && w.u >= w.u_end) done = load_acquire(ticket);
         done = __shfl_sync(0xFFFFFFFFu, done, 0);
+        __syncwarp();  // what lane 0 has acquired is the warp's
         if (done == pieces - 1) {
           for (int i = 0; i < pieces; ++i)
             if (i != index) add(i, true);

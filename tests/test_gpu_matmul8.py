@@ -179,6 +179,47 @@ def test_matmul8_strides(mm, T, N, K):
         assert bool((wide[:, :off] == 7).all()) and bool((wide[:, off + N:] == 7).all())
 
 
+def test_matmul8_bytes_views_and_nothing(mm):
+    """Tensors of bytes, a column of a wider tensor as the scales per row, and calls without rows or columns."""
+    p = Product(33, 300, 528, row_scale=True)
+    want = p.forward(mm).clone()
+    wide = torch.full((33, 5), 9.0, device="cuda")
+    wide[:, 3:4] = p.a_scales
+    p.a8, p.w8, p.a_scales = p.a8.view(torch.uint8), p.w8.view(torch.uint8), wide[:, 3:4]
+    p.out = torch.zeros_like(p.out)
+    assert torch.equal(p.forward(mm), want)
+    p.w8, p.w_scales, p.out = p.w8[:0], p.w_scales[:0], p.out[:, :0]
+    p.forward(mm)
+    assert mm.get_error() == 0
+
+
+def test_matmul8_beside_attention(mm):
+    """A product and an attention call on two streams at once, both of which fill tensor memory."""
+    attn = rel.PagedAttention(device=0)
+    p = Product(200, 4000, 4096)
+    g = gen(3)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF16)
+    k, v, q = rand(40, 64, 2, 128), rand(40, 64, 2, 128), rand(300, 16, 128)
+    table = torch.arange(40, dtype=torch.int32, device="cuda")[None]
+    start = torch.tensor([0, 300], dtype=torch.int32, device="cuda")
+    kv = torch.tensor([2500], dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    call = lambda s=None: attn.forward(q, k, v, table, start, kv, out, scale=0.1, stream=s)
+    call()
+    want = p.forward(mm).clone(), out.clone()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(10):
+        p.out.zero_(), out.zero_()
+        torch.cuda.synchronize()
+        for _ in range(5):
+            p.forward(mm, stream=a)
+            call(b)
+        torch.cuda.synchronize()
+        assert torch.equal(p.out, want[0]) and torch.equal(out, want[1])
+    assert mm.get_error() == 0 and attn.get_error() == 0
+    attn.close()
+
+
 @pytest.mark.parametrize("T", [4, 200, 700])
 def test_matmul8_odd_values(mm, T):
     """NaN and infinite scales and NaN values reach their row or column and no other; zeros and huge scales."""

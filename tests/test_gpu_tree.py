@@ -310,6 +310,23 @@ def test_tree_attention_does_not_write_beyond_its_requests(handle):
     assert torch.equal(wide[:15], c.forward(handle))
 
 
+def test_tree_attention_strides_and_nothing(handle):
+    """q and out inside wider rows, a table of wider rows; calls without tokens or requests write nothing."""
+    c = Case([40, 130, 3], [20, 50, 7], 8, 2, 64, 16, 2, masks="tree", seed=30)
+    want = c.check(handle)
+    wide = torch.full((77, 8, 192), 2.0, dtype=BF16, device="cuda")
+    wide[:, :, :64] = c.q
+    c.q = wide[:, :, :64]
+    table = torch.nn.functional.pad(c.table, (1, 3), value=-1)
+    c.table = table[:, 1:1 + c.table.shape[1]]
+    out = wide[:, :, 128:]
+    c.forward(handle, out=out)
+    assert torch.equal(out, want) and bool((wide[:, :, 64:128] == 2).all())
+    handle.forward(c.q[:0], c.k, c.v, c.table, torch.zeros(4, dtype=I32, device="cuda"), c.kv, out[:0], scale=1.0, tree=c.mask[:0])
+    handle.forward(c.q, c.k, c.v, c.table[:0], c.q_start[:1], c.kv[:0], out, scale=1.0, tree=c.mask)
+    assert torch.equal(out, want) and handle.get_error() == 0
+
+
 def test_tree_attention_refusals(handle):
     c = Case([20], [6], 4, 1, 64, 16, 1, seed=1)
     for bad in (c.mask[:5], c.mask.long(), c.mask.flatten(), c.mask.cpu(), torch.zeros(6, 2, dtype=I32, device="cuda")[:, ::2]):
