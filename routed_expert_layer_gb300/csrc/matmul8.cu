@@ -251,15 +251,16 @@ cudaError_t quantize(const moe_quantize8_args& a, cudaStream_t s) {
 // of 8 units at a time to shared memory (rows of scales are read along K, the epilogue wants them down the rows). 4..11:
 // epilogue, a thread per row, half of the tile's columns each.
 //
-// Measured (bf16; the weights of a call not in L2). 8192 x 14336 x 7168 (tokens, outputs, K): 708 to 727 us, 2.3 to 2.4 PFLOP/s, 1.2
+// Measured (bf16; the weights of a call not in L2). 8192 x 14336 x 7168 (tokens, outputs, K): 708 to 741 us, 2.3 to 2.4 PFLOP/s, 1.2
 // times the bf16 rate. A pair's unit takes some 1,050 cycles where its products alone take 521 and its copies 660 (the copies
 // with one MMA in four and no epilogue); without the loads of tensor memory 842: TMA's writes, the MMAs' operands, the
 // epilogue's loads and every look at a barrier share the SM's memories, and no unit of it is full (tensor pipe 51 %, issue 41 %).
-// 53 x 14336 x 7168: 24 us, 4.4 TB/s (no work in the epilogue: 21); 1 x 7168 x 12288 23.4 us. Bound by a unit's chain of
-// accesses to shared memory, each some 150 cycles while copies and MMAs keep it busy.
+// 53 x 14336 x 7168: 21.3 us, 4.9 TB/s; 1 x 7168 x 12288 20.7 us. Their 112 CTAs stream at 5.9 TB/s after a start of 2.4 us; before
+// two units were handed over at once, a unit's chain of accesses to shared memory bound them (each some 150 cycles while
+// copies and MMAs keep it busy).
 // On the way, 4096 x 14336 x 7168 (361 us): every arrival on the other CTA released at cluster scope, which waits for the
 // thread's stores, 1033; addresses spilled in the units' loop 384; steps of 128 columns with half a warp's columns in each 510;
-// scalar products 392; one lane polling for its warp 424. 53 x 14336 x 7168: weights in the lanes and tokens in the columns 31 us
+// scalar products 392; one lane polling for its warp 424. 53 x 14336 x 7168 (23.9 then): weights in the lanes and tokens in the columns 31 us
 // (a scale per column comes from shared memory; one token 25.1, then 26.9); tiles of 96 rows of W8, so that 150 CTAs work, 28.8;
 // the next unit's scales read early 26.8.
 
@@ -291,13 +292,16 @@ struct MatmulCfg {
   static constexpr int kThreads = 128 + 32 * kEpi;
   static constexpr int kBlocks = BN / 128;         // blocks of W8's scales in a tile
   static constexpr int kBufs = 4;                  // products of 128 columns in tensor memory
-  static constexpr int kDeep = kBufs / kBlocks;    // of units
+  // Units whose products are handed to the epilogue at once. A look at a barrier costs it some 150 cycles, so where tensor
+  // memory holds four units it is every other (53 x 14336 x 7168: 21.3 us for 23.9).
+  static constexpr int kGroup = CG == 1 ? 2 : 1;
+  static constexpr int kDeep = kBufs / kBlocks / kGroup;  // groups in tensor memory
   static constexpr int kPart = 128 * BN;
   static constexpr int kB = 128 * 128;             // bytes of W8 in a stage: 128 rows per CTA
   static_assert(BN == 128 * CG, "each CTA of a tile loads 128 rows of W8");
   static constexpr int kStaging = kEpi * 4096;
   static constexpr int kMaxStages = 12;
-  static constexpr double kUnitUs = CG == 1 ? 0.34 : 0.54;  // a unit's time on the SM
+  static constexpr double kUnitUs = CG == 1 ? 0.30 : 0.54;  // a unit's time on the SM
   static constexpr int kScales = kChunk * (kScaleRow + BN / 128);  // floats of a chunk's scales
   // Shared memory. What the epilogue uses lies at constant places: addresses cost it no registers, and a spilled one in the
   // units' loop costs more than the arithmetic there.
@@ -447,7 +451,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const int e = warp - 4, quarter = warp & 3, part = e >> 2, block = CG == 1 ? 0 : part;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     uint8_t* stage = smem + C::kStagingAt + e * 4096;
-    uint32_t units = 0, chunks = 0;  // passed so far: their buffers and parities
+    uint32_t groups = 0, chunks = 0;  // passed so far: their buffers and parities
     const uint32_t first_empty = CG == 1 ? 0 : cluster_addr(acc_empty, 0);
     const auto free_acc = [&](uint32_t at) {
       if constexpr (CG == 1) mbar_arrive(&acc_empty[at]);
@@ -471,38 +475,50 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < C::kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
 #pragma unroll 1
-      for (int k = 0; k < count; ++k, ++units) {
-        const int x = k & (kChunk - 1), buf = units % C::kDeep * C::kBlocks + block;
+      for (int k = 0; k < count; k += C::kGroup, ++groups) {
+        const int x = k & (kChunk - 1), bar_at = groups % C::kDeep * C::kBlocks + block;
         if (x == 0) ok = wait_warp(&scale_full[chunks & 1], chunks >> 1 & 1, p.err);
         const float* sc = scales + (chunks & 1) * C::kScales;
-        const float s = sc[x * kScaleRow + quarter * 32 + lane] * sc[kChunk * kScaleRow + x * C::kBlocks + block];
-        ok = ok && wait_warp(&acc_full[buf], units / C::kDeep & 1, p.err);
+        float s[C::kGroup];
+#pragma unroll
+        for (int u = 0; u < C::kGroup; ++u)
+          s[u] = sc[(x + u) * kScaleRow + quarter * 32 + lane] * sc[kChunk * kScaleRow + (x + u) * C::kBlocks + block];
+        ok = ok && wait_warp(&acc_full[bar_at], groups / C::kDeep & 1, p.err);
         if (!ok) break;
         tc_fence_after();
-        if (live) {
-          const uint32_t from = tmem + lane_base + buf * 128 + (CG == 1 ? part * C::kCols : 0);
-          const float2 s2 = make_float2(s, s);
-          uint32_t v[2][32];  // a load runs under the arithmetic of the one before
-          tmem_ld32(from, v[0]);
-#pragma unroll
-          for (int c = 0; c < C::kCols / 32; ++c) {
-            tmem_wait_ld32(v[c & 1]);
-            if (c + 1 < C::kCols / 32) {
-              tmem_ld32(from + (c + 1) * 32, v[(c + 1) & 1]);
-            } else {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) free_acc(buf);
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              acc[c * 16 + i] = fma2(make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), s2, acc[c * 16 + i]);
-          }
-        } else {
+        const auto release = [&] {
+          tc_fence_before();
           __syncwarp();
-          if (lane == 0) free_acc(buf);
+          if (lane == 0) free_acc(bar_at);
+        };
+        if (live) {
+          const uint32_t from = tmem + lane_base + bar_at * C::kGroup * 128 + (CG == 1 ? part * C::kCols : 0);
+          const auto add_units = [&](auto n) {
+            constexpr int kPer = C::kCols / 32, kAll = decltype(n)::value * kPer;  // chunks of 32 columns
+            const auto at = [&](int c) { return from + c / kPer * 128 + c % kPer * 32; };
+            float2 s2[C::kGroup];
+#pragma unroll
+            for (int u = 0; u < C::kGroup; ++u) s2[u] = make_float2(s[u], s[u]);
+            uint32_t v[2][32];  // a load runs under the arithmetic of the one before
+            tmem_ld32(from, v[0]);
+#pragma unroll
+            for (int c = 0; c < kAll; ++c) {
+              tmem_wait_ld32(v[c & 1]);
+              if (c + 1 < kAll) tmem_ld32(at(c + 1), v[(c + 1) & 1]);
+              else release();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float2& sum = acc[c % kPer * 16 + i];
+                sum = fma2(make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), s2[c / kPer], sum);
+              }
+            }
+          };
+          if (C::kGroup == 1 || k + 1 < count) add_units(std::integral_constant<int, C::kGroup>());
+          else add_units(std::integral_constant<int, 1>());
+        } else {
+          release();
         }
-        if (x == kChunk - 1 || k + 1 == count) {
+        if (x == kChunk - C::kGroup || k + C::kGroup >= count) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&scale_empty[chunks & 1]);
           ++chunks;
@@ -639,22 +655,30 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         const uint64_t da = desc_sw128(smem_u32(sa)), dw = desc_sw128(smem_u32(sw));
         uint32_t s = 0, turn = 0, buf = 0, buf_turn = 0;
         while (ok && w.next(p)) {
-          for (int k = w.k0; k < w.k1; ++k) {
-            ok = mbar_wait(&full[s], turn, p.err);
-            const uint64_t a = da + ((uint32_t)(s * a_bytes) >> 4), b = dw + ((uint32_t)(s * C::kB) >> 4);
+          for (int k = w.k0; k < w.k1; k += C::kGroup) {
 #pragma unroll
-            for (int h = 0; h < C::kBlocks; ++h, ++buf) {
-              ok = ok && mbar_wait(&acc_empty[buf], buf_turn ^ 1u, p.err);
+            for (int u = 0; u < C::kGroup; ++u) {
+              if (u && k + u >= w.k1) break;
+              ok = ok && mbar_wait(&full[s], turn, p.err);
+              const uint64_t a = da + ((uint32_t)(s * a_bytes) >> 4), b = dw + ((uint32_t)(s * C::kB) >> 4);
+#pragma unroll
+              for (int h = 0; h < C::kBlocks; ++h) {
+                if (u == 0) ok = ok && mbar_wait(&acc_empty[buf + h], buf_turn ^ 1u, p.err);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t to = tmem + ((buf + h) * C::kGroup + u) * 128;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mma_f8_ss<CG>(to, a + j * 2, b + h * (C::kB >> 5) + j * 2, kId, j > 0);
+                if (h + 1 == C::kBlocks) mma_commit_cg<CG>(&empty[s]);
+                if (C::kGroup == 1) mma_commit_cg<CG>(&acc_full[buf + h]);
+              }
               if (!ok) break;
-              tc_fence_after();
-#pragma unroll
-              for (int j = 0; j < 4; ++j) mma_f8_ss<CG>(tmem + buf * 128, a + j * 2, b + h * (C::kB >> 5) + j * 2, kId, j > 0);
-              if (h + 1 == C::kBlocks) mma_commit_cg<CG>(&empty[s]);
-              mma_commit_cg<CG>(&acc_full[buf]);
+              if (++s == (uint32_t)p.stages) s = 0, turn ^= 1u;
             }
             if (!ok) break;
-            if (buf == C::kBufs) buf = 0, buf_turn ^= 1u;
-            if (++s == (uint32_t)p.stages) s = 0, turn ^= 1u;
+            if (C::kGroup > 1) mma_commit_cg<CG>(&acc_full[buf]);
+            buf += C::kBlocks;
+            if (buf == C::kDeep * C::kBlocks) buf = 0, buf_turn ^= 1u;
           }
         }
         mma_commit_cg<CG>(drain);  // every MMA issued, and every arrival on the other CTA's barriers, is through
@@ -725,8 +749,8 @@ bool matmul8_configure() {
 // tiles left over are cut: every tile into the same number of pieces, or all units into as many stretches as there are CTAs,
 // whose borders then lie inside tiles. The estimates, in us, are of this card: a unit takes what its products do or, of weights
 // that stream from memory, its bytes' share; the pieces of a tile are written and read again; and a stretch that goes on in
-// a second tile stalls for its first piece's way out. (517 x 1811 x 7152: 75 tiles of single CTAs in two pieces each 19.7 us,
-// 24 of pairs in three 23.9; 1024 x 14336 x 7168 119 and 90.)
+// a second tile stalls for its first piece's way out. (517 x 1811 x 7152: 75 tiles of single CTAs in two pieces each 20.0 us,
+// 24 of pairs in three 24.2; 256 x 14336 x 7168 33 and 37; 4096 x 14336 x 7168 407 and 366.)
 struct MatmulPlan {
   int64_t m_tiles, n_tiles;
   int most, left, cuts;
