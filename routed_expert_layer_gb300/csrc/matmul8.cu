@@ -27,8 +27,9 @@ namespace {
 // elements where not. Every value is read once and held in registers between the maximum and its quotient (rows wider than
 // 32,768 and unaligned 128 x 128 blocks are read again), so memory bounds them: 3 bytes an element.
 
-// x / s, as division rounds it. Where s is neither tiny nor huge: Markstein's correction of x * (1 / s) by its remainder,
-// two operations more than the product, instead of some ten.
+// x / s, as division rounds it. Where s is neither tiny nor huge: Markstein's correction of q = x * (1 / s) by its remainder,
+// two operations more than the product, instead of some ten. (The remainder is taken as q s - x: of a zero it is +0,
+// and -0 * (1 / s) added to q keeps q's sign, where x - q s of x = -0 would turn -0 into +0.)
 struct Quotient {
   float s, r;
   bool plain;
@@ -37,7 +38,7 @@ struct Quotient {
   __device__ __forceinline__ float at(float x) const {
     if constexpr (PLAIN) return s == 0.f ? 0.f : x / s;
     const float q = x * r;
-    return fmaf(fmaf(-q, s, x), r, q);
+    return fmaf(fmaf(q, s, -x), -r, q);
   }
   __device__ __forceinline__ uint8_t operator()(float x) const {
     return (uint8_t)(plain ? e4m3x2(at<true>(x), 0.f) : e4m3x2(at<false>(x), 0.f));
