@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         mma_commit_cg<CG>(drain);  // every MMA issued, and every arrival on the other CTA's barriers, is through
       }
       __syncwarp();
-      mbar_wait(drain, 0, p.err);
+      if (rank == 0) mbar_wait(drain, 0, p.err);
     } else {
       uint32_t buf = 0, turn = 0;
       const int x = lane & (kChunk - 1), y = lane / kChunk;  // unit and row of a lane
@@ -723,6 +723,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   else cluster_sync();
   tc_fence_after();
   if (warp == 1) {
+    // The arrival of the last commit on the second CTA's barrier, before its shared memory goes away. The first CTA has seen its own, so
+    // this takes no time; waited for instead of the work, it would give up in a product that runs for longer than a wait may.
+    // (The rank is read again: kept in its register until here, 8192 x 14336 x 7168 takes 760 us instead of 728.)
+    if (CG > 1 && cluster_rank() != 0) mbar_wait(drain, 0, p.err);
     __syncwarp();
     tmem_dealloc_cg<CG>(tmem, 512);
   }

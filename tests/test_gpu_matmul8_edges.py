@@ -2,9 +2,17 @@
 import pytest
 import torch
 
+import routed_expert_layer_gb300 as rel
 from test_gpu_matmul8 import BF16, E4M3, F16, gen, run_quantize
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mm():
+    h = rel.Matmul8(device=0)
+    yield h
+    h.close()
 
 
 @pytest.mark.parametrize("group,rows", [(128, 1), (0, 1), (128, 128)])
@@ -25,3 +33,36 @@ def test_quantize_negative_zeros(group, rows, H, dtype):
     want = torch.where(big > 0, x.float() / big, torch.zeros_like(big)).to(E4M3).view(torch.uint8)
     assert bool((want == 0x80).any()) and bool((want == 0).any()) and bool((want[rows:2 * rows] == 0).all())
     assert torch.equal(out8.view(torch.uint8), want)
+
+
+def test_matmul8_of_seconds(mm):
+    """A product that takes more than two seconds, the time after which a wait inside the kernel gives up: its waits are
+    for a unit of the work each, so no error is raised. Small whole numbers: every sum is exact."""
+    T = N = 458 * 256
+    K = 1832 * 128
+    need = T * K + N * K + 2 * T * N
+    if torch.cuda.mem_get_info()[0] < 1.1 * need:
+        pytest.skip("needs 82 GB of device memory")
+    base = lambda seed: torch.randint(-2, 3, (16, 128), generator=gen(seed), device="cuda").float()
+    a, w = base(1), base(2)
+
+    def spread(t, rows):
+        out = torch.empty(rows, K, dtype=torch.uint8, device="cuda")
+        out.view(rows // 16, 16, K // 128, 128).copy_(t.to(E4M3).view(torch.uint8).view(1, 16, 1, 128))
+        return out
+
+    a8, w8 = spread(a, T), spread(w, N)
+    out = torch.zeros(T, N, dtype=BF16, device="cuda")
+    ones = torch.ones(T, 1, device="cuda")
+    w_ones = torch.ones(N // 128, K // 128, device="cuda")
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    mm.forward(a8, ones, w8, w_ones, out)
+    end.record()
+    assert mm.get_error() == 0
+    assert start.elapsed_time(end) > 2000.0  # (about 2,800 ms)
+    want = ((a.double() @ w.double().t()) * (K // 128)).to(BF16)
+    for rows in out.split(16 * 512):
+        assert bool((rows.view(-1, 16, N // 16, 16) == want.view(1, 16, 1, 16)).all())
+    del a8, w8, out, rows
+    torch.cuda.empty_cache()
