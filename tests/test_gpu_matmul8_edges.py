@@ -2,8 +2,10 @@
 import pytest
 import torch
 
+import draft_reference as dref
+import ops_reference as ref
 import routed_expert_layer_gb300 as rel
-from test_gpu_matmul8 import BF16, E4M3, F16, gen, run_quantize
+from test_gpu_matmul8 import BF16, E4M3, F16, Product, gen, inside, run_quantize
 
 pytestmark = pytest.mark.gpu
 
@@ -33,6 +35,43 @@ def test_quantize_negative_zeros(group, rows, H, dtype):
     want = torch.where(big > 0, x.float() / big, torch.zeros_like(big)).to(E4M3).view(torch.uint8)
     assert bool((want == 0x80).any()) and bool((want == 0).any()) and bool((want[rows:2 * rows] == 0).all())
     assert torch.equal(out8.view(torch.uint8), want)
+
+
+# One CTA a tile, with one row of tiles and with two, and a pair of CTAs (on 152 SMs).
+@pytest.mark.parametrize("T,N,K", [(6, 400, 640), (200, 300, 1168), (1291, 1677, 1040)])
+@pytest.mark.parametrize("row_scale", [False, True])
+def test_matmul8_scales_out_of_range(mm, T, N, K, row_scale):
+    """Scales whose product lies below fp32's normal range or above its largest value."""
+    p = Product(T, N, K, row_scale=row_scale)
+    clean = p.forward(mm).clone()
+    small = lambda r: (torch.randint(0, 8, (r, K), generator=gen(r), device="cuda") +
+                       128 * torch.randint(0, 2, (r, K), generator=gen(r + 1), device="cuda")).to(torch.uint8)  # up to 7 * 2^-9
+    a8, w8 = p.a8.view(torch.uint8), p.w8.view(torch.uint8)
+    a8[:2] &= 0x7F                                  # positive: sums of some 2^20
+    w8[128:256] &= 0x7F
+    p.a_scales[0] = 1.1 * 2.0 ** -72
+    p.a_scales[1] = -1.1 * 2.0 ** -77
+    p.w_scales[1] = 1.27 * 2.0 ** -74               # products of 2^-146 (3 bits left) and 2^-151 (none)
+    a8[2:5] = small(3)
+    w8[:128] = small(128)
+    p.a_scales[2:4] = 1.5 * 2.0 ** 66
+    p.w_scales[0] = 1.25 * 2.0 ** 66                # 2^133: sums of some 2^-10
+    a8[3] = 0                                       # infinity times 0
+    p.a_scales[4] = 0.0
+    p.w_scales[2, 1] = 0.0
+    out = p.forward(mm)
+    want, slack = dref.matmul8(p.a8, p.a_scales, p.w8, p.w_scales)
+    # Below 2^-126 the product of two scales is off by half of 2^-149 at most, and a block's sum is 128 * 448^2 < 2^25 at most.
+    # (Where one is infinite there is no bound to hold: looked at apart.)
+    blocks = -(-K // 128)
+    apart = torch.zeros_like(want, dtype=torch.bool)
+    apart[2:4, :128] = True
+    inside(out.masked_fill(apart, 0.0), want.masked_fill(apart, 0.0), ref.stored(want, BF16, slack + blocks * 2.0 ** -125))
+    assert bool((want[0, 128:256] > 2.0 ** -125).all()) and bool((out[0, 128:256] != 0).all())
+    assert not bool(out[2:4, :128].isfinite().any()) and bool(out[3, :128].isnan().all())
+    assert bool((out[3, 128:] == 0).all()) and bool((out[4] == 0).all())
+    assert torch.equal(out[5:, 384:], clean[5:, 384:])  # rows and columns whose scales and values are as they were
+    assert mm.get_error() == 0
 
 
 def test_matmul8_of_seconds(mm):
