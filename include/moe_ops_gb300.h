@@ -280,7 +280,7 @@ MOE_API int moe_quantize8(void* stream, const moe_quantize8_args* a);
  * rows of every tensor may be strided. K a multiple of 16, a8 and w8 16-byte aligned with row strides that
  * are multiples of 16; out is aligned to its elements. The memory from out's first to its last element
  * overlaps no input's.
- * 0 <= T, N <= 2^30 (T or N 0: nothing is done), 16 <= K <= 2^20. */
+ * 0 <= T, N <= 2^30 (T or N 0: nothing is done), 16 <= K <= 2^20, ceil(T / 128) * ceil(N / 128) <= 2^30. */
 typedef struct {
   const uint8_t* a8;
   const float* a_scales;

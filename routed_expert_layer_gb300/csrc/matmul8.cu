@@ -795,8 +795,7 @@ int matmul8_launch(const moe_matmul8_ctx* ctx, const moe_matmul8_args& a, const 
   MatmulParams p;
   p.a = a;
   p.kb = (a.K + 127) / 128;
-  const int64_t tiles = plan.m_tiles * plan.n_tiles;
-  if (tiles * p.kb >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+  const int64_t tiles = plan.m_tiles * plan.n_tiles;  // (2^30 at most: matmul8_check)
   p.m_tiles = (int)plan.m_tiles;
   p.n_tiles = (int)plan.n_tiles;
   p.whole = (int)tiles - plan.left;
@@ -860,12 +859,13 @@ int matmul8_check(const moe_matmul8_args* a) {
     return MOE_ERR_INVALID_ARG;
   const int blocks = (a->K + 127) / 128;
   if (a->a_blocks != blocks && a->a_blocks != 1) return MOE_ERR_INVALID_ARG;
-  if (a->K > 1 << 20 || a->T > 1 << 30 || a->N > 1 << 30) return MOE_ERR_UNSUPPORTED;
+  const int64_t wb = ((int64_t)a->N + 127) / 128;
+  if (a->K > 1 << 20 || a->T > 1 << 30 || a->N > 1 << 30 || ((int64_t)a->T + 127) / 128 * wb > 1 << 30)
+    return MOE_ERR_UNSUPPORTED;
   if (a->T == 0 || a->N == 0) return MOE_OK;
   if (!a->a8 || !a->w8 || !a->a_scales || !a->w_scales || !a->out || !is_aligned(a->a8, 16) || !is_aligned(a->w8, 16) ||
       !is_aligned(a->a_scales, 4) || !is_aligned(a->w_scales, 4) || !is_aligned(a->out, 2))
     return MOE_ERR_INVALID_ARG;
-  const int64_t wb = ((int64_t)a->N + 127) / 128;
   const auto short_rows = [](int64_t rows, int64_t stride, int64_t width) { return rows > 1 && stride < width; };
   if (short_rows(a->T, a->a8_stride, a->K) || short_rows(a->N, a->w8_stride, a->K) || short_rows(a->T, a->out_stride, a->N) ||
       short_rows(a->T, a->a_scales_stride, a->a_blocks) || short_rows(wb, a->w_scales_stride, blocks) ||
@@ -944,8 +944,8 @@ int moe_matmul8_create(int device, moe_matmul8_ctx** out) {
 }
 
 int moe_matmul8_forward(moe_matmul8_ctx* ctx, void* stream, const moe_matmul8_args* a) {
-  if (!ctx) return MOE_ERR_INVALID_ARG;
   const int st = matmul8_check(a);
+  if (st == MOE_OK && !ctx) return MOE_ERR_INVALID_ARG;
   if (st != MOE_OK || a->T == 0 || a->N == 0) return st;
   DeviceGuard g(ctx->device);
   return a->dtype == MOE_DT_BF16 ? matmul8_by_rows<MOE_DT_BF16>(ctx, *a, (cudaStream_t)stream)
