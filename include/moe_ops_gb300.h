@@ -209,7 +209,7 @@ MOE_API int moe_tree_plan(void* stream, const moe_tree_plan_args* a);
  * row t sees the c = kv_lens - new cached keys and new key j where bit j of mask[n] is set (any
  * bits: a row need not see itself, bits from the number of new tokens on are ignored); of a longer one
  * it sees keys j <= c + t. A row that sees nothing gets zeros and lse = -inf. mask int32
- * [N][words]; everything else as in moe_attn_forward. */
+ * [N][words], which shares no element with out or lse; everything else as in moe_attn_forward. */
 MOE_API int moe_attn_forward_tree(moe_attn_ctx* ctx, void* stream, const moe_attn_args* a, const int32_t* mask,
                                   int32_t words);
 

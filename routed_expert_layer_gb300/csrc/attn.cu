@@ -1150,6 +1150,21 @@ bool shares_elements(const moe_attn_args* a) {
   return false;
 }
 
+// Whether the bytes in [lo, hi) hold an element of out (they may lie between its rows or heads) or of lse.
+bool meets_outputs(const moe_attn_args* a, const char* lo, const char* hi) {
+  const Span mask = {lo, hi}, lse = {(const char*)a->lse, (const char*)(a->lse + (a->lse ? (int64_t)a->N * a->Hq : 0))};
+  if (overlap(mask, lse)) return true;
+  if (!overlap(mask, span16(a->out, a->N, a->out_tok, a->Hq, a->out_head, a->D))) return false;
+  const int64_t row = 2 * (int64_t)a->D, apart = a->N > 1 ? 2 * a->out_tok : 1;
+  for (int64_t h = 0; h < a->Hq; ++h) {
+    const char* first = (const char*)a->out + (a->Hq > 1 ? 2 * h * a->out_head : 0);
+    const int64_t below = lo - row - first;  // the first token whose row ends behind lo
+    const int64_t n = below < 0 ? 0 : below / apart + 1;
+    if (n < a->N && first + n * apart < hi) return true;
+  }
+  return false;
+}
+
 int attn_check(const moe_attn_args* a) {
   if (!a || a->N < 0 || a->B < 0 || a->Hq < 1 || a->Hkv < 1 || a->Hq % a->Hkv || a->num_pages < 1 || a->W < 1 ||
       a->max_new < 0 || !is_pow2(a->page_size) || a->table_stride < a->W)
@@ -1263,6 +1278,7 @@ int moe_attn_forward_tree(moe_attn_ctx* ctx, void* stream, const moe_attn_args* 
   if (words > MOE_TREE_WORDS) return MOE_ERR_UNSUPPORTED;
   if (a->N == 0 || a->B == 0) return MOE_OK;
   if (!mask || !is_aligned(mask, 4)) return MOE_ERR_INVALID_ARG;
+  if (meets_outputs(a, (const char*)mask, (const char*)(mask + (int64_t)a->N * words))) return MOE_ERR_INVALID_ARG;
   return attn_forward(ctx, stream, a, mask, words);
 }
 
