@@ -45,3 +45,18 @@ def test_tree_attention_mask_in_outputs(handle):
     both = torch.empty(2 * N, dtype=I32, device="cuda")
     call(at(both, N), out)
     assert torch.equal(out, want) and handle.get_error() == 0
+
+
+@pytest.mark.parametrize("ctx,new,Hq,Hkv,D,words", [
+    ([700, 3], [33, 90], 24, 2, 128, 1), ([64, 1000, 0], [130, 65, 100], 8, 1, 64, 2), ([40, 500], [40, 60], 2, 2, 64, 1),
+    ([300, 9], [300, 20], 12, 1, 128, 8),
+])
+def test_tree_attention_chunks_longer_than_the_mask(handle, ctx, new, Hq, Hkv, D, words):
+    """Requests of more new tokens than the mask has bits see what is before them, beside trees or alone; max_new picks the same
+    variant as the number of all tokens here, so it changes no bit."""
+    c = Case(ctx, new, Hq, Hkv, D, 16, words, masks="tree", seed=sum(new))
+    assert max(new) > 32 * words
+    a = c.check(handle)
+    assert torch.equal(a, c.check(handle, max_new=max(new)))
+    if min(new) > 32 * words:  # no request with a tree: what the call without masks computes
+        assert torch.equal(a, c.check(handle, mask=False))
