@@ -25,7 +25,8 @@ namespace {
 
 // Three kernels by the shape of a block, each with 16-byte loads where widths, strides and addresses allow it and single
 // elements where not. Every value is read once and held in registers between the maximum and its quotient (rows wider than
-// 32,768 and unaligned 128 x 128 blocks are read again), so memory bounds them: 3 bytes an element.
+// 32,768, or than 4,096 where they go by single elements, and unaligned 128 x 128 blocks are read again), so memory bounds them: 3 bytes
+// an element.
 
 // x / s, as division rounds it. Where s is neither tiny nor huge: Markstein's correction of q = x * (1 / s) by its remainder,
 // two operations more than the product, instead of some ten. (The remainder is taken as q s - x: of a zero it is +0,
@@ -134,7 +135,8 @@ __device__ __forceinline__ uint32_t threads_max(uint32_t m, bool one_warp, uint3
   return m;
 }
 
-// Whole rows: a row per block, or per warp (blockDim.y of them).
+// Whole rows: a row per block, or per warp (blockDim.y of them). 8192 x 12288, bf16: 64 us, 4.7 TB/s; 8192 x 12289, by single elements and read
+// twice, 197 us.
 template <int DT, bool WIDE>
 __global__ void __launch_bounds__(1024) quantize_rows_kernel(const moe_quantize8_args a) {
   constexpr int kHeld = 4, kPiece = WIDE ? 8 : 1;
@@ -171,7 +173,7 @@ __global__ void __launch_bounds__(1024) quantize_rows_kernel(const moe_quantize8
   }
 }
 
-// Blocks of 128 x 128: one per thread block, 8 pieces of 8 elements per thread.
+// Blocks of 128 x 128: one per thread block, 8 pieces of 8 elements per thread. 14336 x 7168, bf16: 52 us, 5.9 TB/s.
 template <int DT, bool WIDE>
 __global__ void __launch_bounds__(256) quantize_tiles_kernel(const moe_quantize8_args a, int nb) {
   __shared__ uint32_t red[32];
@@ -252,14 +254,15 @@ cudaError_t quantize(const moe_quantize8_args& a, cudaStream_t s) {
 // of 8 units at a time to shared memory (rows of scales are read along K, the epilogue wants them down the rows). 4..11:
 // epilogue, a thread per row, half of the tile's columns each.
 //
-// Measured (bf16; the weights of a call not in L2). 8192 x 14336 x 7168 (tokens, outputs, K): 708 to 741 us, 2.3 to 2.4 PFLOP/s, 1.2
+// Measured (bf16; the weights of a call not in L2). 8192 x 14336 x 7168 (tokens, outputs, K): 721 to 738 us, 2.3 PFLOP/s, 1.2
 // times the bf16 rate. A pair's unit takes some 1,050 cycles where its products alone take 521 and its copies 660 (the copies
 // with one MMA in four and no epilogue); without the loads of tensor memory 842: TMA's writes, the MMAs' operands, the
 // epilogue's loads and every look at a barrier share the SM's memories, and no unit of it is full (tensor pipe 51 %, issue 41 %).
-// 53 x 14336 x 7168: 21.3 us, 4.9 TB/s; 1 x 7168 x 12288 20.7 us. Their 112 CTAs stream at 5.9 TB/s after a start of 2.4 us; before
+// 53 x 14336 x 7168: 21.3 us, 4.9 TB/s; 1 x 7168 x 12288 20.6 us. Their 112 CTAs stream at 5.9 to 6.6 TB/s beside some 4 us for the start
+// and the end (53 tokens, 14,336 outputs, K of 3,584, 7,168, 14,336 and 28,672: 12.7, 21.3, 37.1 and 69.3 us); before
 // two units were handed over at once, a unit's chain of accesses to shared memory bound them (each some 150 cycles while
 // copies and MMAs keep it busy).
-// On the way, 4096 x 14336 x 7168 (361 us): every arrival on the other CTA released at cluster scope, which waits for the
+// On the way, 4096 x 14336 x 7168 (361 us then): every arrival on the other CTA released at cluster scope, which waits for the
 // thread's stores, 1033; addresses spilled in the units' loop 384; steps of 128 columns with half a warp's columns in each 510;
 // scalar products 392; one lane polling for its warp 424. 53 x 14336 x 7168 (23.9 then): weights in the lanes and tokens in the columns 31 us
 // (a scale per column comes from shared memory; one token 25.1, then 26.9); tiles of 96 rows of W8, so that 150 CTAs work, 28.8;
@@ -756,8 +759,8 @@ bool matmul8_configure() {
 // tiles left over are cut: every tile into the same number of pieces, or all units into as many stretches as there are CTAs,
 // whose borders then lie inside tiles. The estimates, in us, are of this card: a unit takes what its products do or, of weights
 // that stream from memory, its bytes' share; the pieces of a tile are written and read again; and a stretch that goes on in
-// a second tile stalls for its first piece's way out. (517 x 1811 x 7152: 75 tiles of single CTAs in two pieces each 20.0 us,
-// 24 of pairs in three 24.2; 256 x 14336 x 7168 33 and 37; 4096 x 14336 x 7168 407 and 366.)
+// a second tile stalls for its first piece's way out. (517 x 1811 x 7152: 75 tiles of single CTAs in two pieces each 19.8 us,
+// 24 of pairs in three 24.1; 256 x 14336 x 7168 33.5 and 36.7; 4096 x 14336 x 7168 395 and 363.)
 struct MatmulPlan {
   int64_t m_tiles, n_tiles;
   int most, left, cuts;

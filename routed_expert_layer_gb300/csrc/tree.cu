@@ -76,7 +76,8 @@ __global__ void __launch_bounds__(kTreeNodes) tree_plan_kernel(const moe_tree_pl
     }
     up = next;
   }
-  // chunks by the whole block (the loop above has synchronised it)
+  // chunks by the whole block (the loop above has synchronised it): 16 trees take 2.3 us, beside a chunk of 2,048 tokens 2.3, of 8,192 4.3, of
+  // 60,000 21
   for (int g = 0; g < kTreeNodes >> per_shift; ++g) {
     const int tokens = s_chunk[g][0], row = s_chunk[g][1], from = s_chunk[g][2];
 #pragma unroll 4
