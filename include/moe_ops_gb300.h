@@ -274,9 +274,9 @@ MOE_API int moe_quantize8(void* stream, const moe_quantize8_args* a);
  * from left to right in fp32: the product of the two scales is formed first, the products of a block are summed by
  * the tensor cores, and the blocks are added up; out is rounded once to dtype. So a product of scales below 2^-126 is
  * rounded to a multiple of 2^-149, by which a block's term is off by 2^-125 at most, and one of 2^128 or more is infinite and
- * makes the term infinite, or NaN where the block's sum is 0. a8 [T][K], w8 [N][K] (a library layer's [out][in]), out [T][N]; w_scales
- * [ceil(N / 128)][ceil(K / 128)]; a_scales [T][a_blocks], a_blocks = ceil(K / 128), or 1 for a
- * scale per row. The scales are as moe_add_rmsnorm (group 0, 128) and moe_quantize8 write them;
+ * makes the term infinite, or NaN where the block's sum is 0.
+ * a8 [T][K], w8 [N][K] (a library layer's [out][in]), out [T][N]; w_scales [ceil(N / 128)][ceil(K / 128)];
+ * a_scales [T][a_blocks], a_blocks = ceil(K / 128), or 1 for a scale per row. The scales are as moe_add_rmsnorm (group 0, 128) and moe_quantize8 write them;
  * rows of every tensor may be strided. K a multiple of 16, a8 and w8 16-byte aligned with row strides that
  * are multiples of 16; out is aligned to its elements. The memory from out's first to its last element
  * overlaps no input's.

@@ -483,8 +483,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         const int x = k & (kChunk - 1), bar_at = groups % C::kDeep * C::kBlocks + block;
         if (x == 0) ok = wait_warp(&scale_full[chunks & 1], chunks >> 1 & 1, p.err);
         const float* sc = scales + (chunks & 1) * C::kScales;
-        // The product of the scales first, as the interface says it: scales whose product leaves fp32's range while the term does not cost
-        // every other call a look at each chunk (8192 x 14336 x 7168 765 us for 722, 1 x 7168 x 12288 21.0 for 20.6).
+        // The product of the scales first, as the interface says it. (The sum times one scale after the other, in chunks where that product
+        // leaves fp32's range, costs every call a look at each chunk: 8192 x 14336 x 7168 765 us for 722, 1 x 7168 x 12288 21.0 for 20.6.)
         float s[C::kGroup];
 #pragma unroll
         for (int u = 0; u < C::kGroup; ++u)

@@ -137,9 +137,9 @@ class Matmul8:
 
     def forward(self, a8, a_scales, w8, w_scales, out, stream=None) -> None:
         """out[t][n] = sum over blocks of 128 of a_scales[t][b] w_scales[n / 128][b] (a8 w8^T of the block)
-        (moe_matmul8_forward; the product of the two scales is formed first, in fp32). a8 [T][K], w8 [N][K]: float8_e4m3fn or uint8, K a multiple of 16; a_scales
-        float32 [T][ceil(K/128)] or [T][1]; w_scales float32 [ceil(N/128)][ceil(K/128)]; out bf16 or f16
-        [T][N]. Rows may be strided (a8 and w8: by multiples of 16, from 16-byte aligned addresses)."""
+        (moe_matmul8_forward; the product of the two scales is formed first, in fp32). a8 [T][K], w8 [N][K]:
+        float8_e4m3fn or uint8, K a multiple of 16; a_scales float32 [T][ceil(K/128)] or [T][1]; w_scales float32
+        [ceil(N/128)][ceil(K/128)]; out bf16 or f16 [T][N]. Rows may be strided (a8 and w8: by multiples of 16, from 16-byte aligned addresses)."""
         if not self.ctx:
             raise ValueError("the handle is closed")
         st = _matmul8(self.ctx.value, self.device, a8, a_scales, w8, w_scales, out, stream)
@@ -182,8 +182,8 @@ class PagedAttention:
         """out[n] = attention of q[n] over its request's keys up to its own position
         (moe_attn_forward), or with tree int32 [N][words] (tree_plan's mask) over the cached keys and those new
         tokens whose bits are set (moe_attn_forward_tree; a request with more than 32 * words new tokens is a
-        plain chunk; tree shares no memory with out or lse). q, out [N][Hq][D]; caches [pages][P][Hkv][D] (any strides, D
-        contiguous); block_table int32 [B][W], q_start int32 [B+1], kv_lens int32 [B]; lse
+        plain chunk; tree shares no memory with out or lse). q, out [N][Hq][D]; caches [pages][P][Hkv][D] (any
+        strides, D contiguous); block_table int32 [B][W], q_start int32 [B+1], kv_lens int32 [B]; lse
         float32 [N][Hq], contiguous, or None; max_new: the most new tokens of a request, if
         known (picks a variant)."""
         if not self.ctx:
